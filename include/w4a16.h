@@ -355,9 +355,130 @@ w4a16_status w8a8_quantize_activations(const void* X, int64_t M, int64_t K, void
 w4a16_status w8a8_gemm(const void* qx, const void* sx, int64_t M, int64_t K, const void* qw,
                        const void* sw, int64_t N, void* Y, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the quantized linear layer: the gated feed-forward block, gradients for
+ * training through fixed or freshly quantized weights, and the embedding.
+ * Quantized weights are those of w4a16_quantize (w8a16_quantize for the w8a16_
+ * forms): same layouts, g and K rules, alignment, stream and error conventions as
+ * above, and the weight they stand for is the same Ŵ = bf16_rn((q − z)·s).
+ * Every product is accumulated in binary32.  Results are deterministic.  Every
+ * workspace is scratch: calls that may run at the same time (two streams, two
+ * captured graphs) need two.
+ * ------------------------------------------------------------------------- */
+
+/* Activations of the gated block. */
+typedef enum w4a16_act {
+    W4A16_ACT_SILU = 0,       /* x / (1 + e^-x) */
+    W4A16_ACT_GELU = 1,       /* x·Φ(x), Φ the normal distribution function */
+    W4A16_ACT_GELU_TANH = 2,  /* x/2·(1 + tanh(√(2/π)·(x + 0.044715·x³))) */
+    W4A16_ACT_RELU = 3        /* max(x, 0) */
+} w4a16_act;
+
+/* Bytes of device workspace w4a16_gated needs for this shape and path (0 for
+ * rejected shapes).  Uses the current device's SM count. */
+size_t w4a16_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t g, int32_t path);
+size_t w8a16_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t g, int32_t path);
+
+/* Gated feed-forward block: G = X·Ŵgateᵀ, U = X·Ŵupᵀ, H = bf16_rn(act(G)·U), in one
+ * kernel: the projections meet in binary32 and only H is written.
+ *   X bf16 [M, K]; gate and up weights [N, K] each; H out bf16 [M, N].
+ *   G, U out bf16 [M, N], both or neither (NULL): the projections, each rounded once,
+ *   as w4a16_gated_backward takes them.
+ *   path: w4a16_path, optionally OR'ed with W4A16_STATIC_WEIGHTS (M ≤ 16); AUTO runs
+ *   the decode kernel for M ≤ 16 (every weight is read once at HBM rate), else the
+ *   tensor-core kernel. */
+w4a16_status w4a16_gated(const void* X, int64_t M, int64_t K, const void* gate_packed,
+                         const void* gate_scales, const void* gate_zeros, const void* up_packed,
+                         const void* up_scales, const void* up_zeros, int64_t N, int32_t g,
+                         int32_t sym, int32_t act, void* H, void* G, void* U, void* workspace,
+                         size_t workspace_bytes, int32_t path, void* stream);
+w4a16_status w8a16_gated(const void* X, int64_t M, int64_t K, const void* gate_codes,
+                         const void* gate_scales, const void* gate_zeros, const void* up_codes,
+                         const void* up_scales, const void* up_zeros, int64_t N, int32_t g,
+                         int32_t sym, int32_t act, void* H, void* G, void* U, void* workspace,
+                         size_t workspace_bytes, int32_t path, void* stream);
+
+/* Bytes of device workspace of w4a16_gated_backward and w8a16_gated_backward. */
+size_t w4a16_gated_backward_workspace_size(int64_t M, int64_t N, int64_t K, int32_t g);
+
+/* Backward pass of the gated block for a gradient dH of H:
+ *   dG = bf16_rn(dH·U·act'(G)),  dU = bf16_rn(dH·act(G)),  dX = bf16_rn(dG·Ŵgate + dU·Ŵup).
+ *   dH, G, U in bf16 [M, N] (G and U as w4a16_gated keeps them); dG, dU out bf16
+ *   [M, N]: the gradients at the projections' outputs, from which w4a16_gemm_wgrad
+ *   (or an adapter) goes on; dX out bf16 [M, K].  dG and dU may be G's and U's own
+ *   buffers.  The products are formed from the rounded dG and dU.  N = 0 gives dX = 0. */
+w4a16_status w4a16_gated_backward(const void* dH, const void* G, const void* U, int64_t M,
+                                  int64_t N, const void* gate_packed, const void* gate_scales,
+                                  const void* gate_zeros, const void* up_packed,
+                                  const void* up_scales, const void* up_zeros, int64_t K,
+                                  int32_t g, int32_t sym, int32_t act, void* dX, void* dG,
+                                  void* dU, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+w4a16_status w8a16_gated_backward(const void* dH, const void* G, const void* U, int64_t M,
+                                  int64_t N, const void* gate_codes, const void* gate_scales,
+                                  const void* gate_zeros, const void* up_codes,
+                                  const void* up_scales, const void* up_zeros, int64_t K,
+                                  int32_t g, int32_t sym, int32_t act, void* dX, void* dG,
+                                  void* dU, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Bytes of device workspace of w4a16_gemm_dgrad and w8a16_gemm_dgrad. */
+size_t w4a16_gemm_dgrad_workspace_size(int64_t M, int64_t N, int64_t K, int32_t g);
+
+/* Gradient of Y = X·Ŵᵀ with respect to X: dX[M, K] = bf16_rn(dY[M, N]·Ŵ[N, K]), from
+ * the packed codes as they are stored (Ŵ is formed on chip, never transposed in
+ * memory).  N = 0 gives dX = 0. */
+w4a16_status w4a16_gemm_dgrad(const void* dY, int64_t M, int64_t N, const void* packed,
+                              const void* scales, const void* zeros, int64_t K, int32_t g,
+                              int32_t sym, void* dX, void* workspace, size_t workspace_bytes,
+                              void* stream);
+w4a16_status w8a16_gemm_dgrad(const void* dY, int64_t M, int64_t N, const void* codes,
+                              const void* scales, const void* zeros, int64_t K, int32_t g,
+                              int32_t sym, void* dX, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Bytes of device workspace of w4a16_gemm_wgrad (0 unless N needs padding to 8). */
+size_t w4a16_gemm_wgrad_workspace_size(int64_t M, int64_t N);
+
+/* Gradient of a linear layer with respect to its dense weight: dW[N, K] =
+ * bf16_rn(dY[M, N]ᵀ·X[M, K]).  For weights quantized in every step this is the
+ * straight-through gradient of the weight that was quantized.  K must be a multiple of
+ * 32; any N.  M = 0 gives dW = 0. */
+w4a16_status w4a16_gemm_wgrad(const void* dY, const void* X, int64_t M, int64_t N, int64_t K,
+                              void* dW, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Embedding from a quantized table [V, K]: out[t, :] = bf16_rn(scale·Ŵ[ids[t], :]).
+ *   ids in int32 or int64 [T] (id_bytes 4 or 8); out bf16 [T, K].
+ * An id below 0 is padding and gives a row of zeros.  An id not below V gives a row of
+ * zeros too and sets the device error word to W4A16_DEVERR_ID. */
+w4a16_status w4a16_embedding(const void* ids, int32_t id_bytes, int64_t T, const void* packed,
+                             const void* scales, const void* zeros, int64_t V, int64_t K,
+                             int32_t g, int32_t sym, float scale, void* out, void* stream);
+w4a16_status w8a16_embedding(const void* ids, int32_t id_bytes, int64_t T, const void* codes,
+                             const void* scales, const void* zeros, int64_t V, int64_t K,
+                             int32_t g, int32_t sym, float scale, void* out, void* stream);
+
+/* Bytes of device workspace w4a16_embedding_grad needs. */
+size_t w4a16_embedding_grad_workspace_size(int64_t T, int64_t V, int64_t K);
+
+/* Gradient of the dense table [V, K] behind an embedding (straight through the
+ * quantizer): dW[v, :] = scale·Σ_{t: ids[t] = v} dY[t, :], summed in binary32 over the
+ * tokens sorted by id, in a fixed order; rows that no token names are written as zeros.
+ *   dY bf16 [T, K], K a multiple of 32; dW out [V, K], binary32 (f32 = 1) or bf16 (0).
+ * Ids below 0 are padding and add nothing; so do ids not below V, which set the device
+ * error word to W4A16_DEVERR_ID. */
+w4a16_status w4a16_embedding_grad(const void* dY, const void* ids, int32_t id_bytes, int64_t T,
+                                  int64_t V, int64_t K, float scale, int32_t f32, void* dW,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device error word: what a kernel reported. */
+#define W4A16_DEVERR_WAIT 1   /* a bounded wait was given up */
+#define W4A16_DEVERR_ID 2     /* an embedding met an id not below the table's rows */
+
 /* Read and clear the current device's error word, written by a kernel that gave
  * up a bounded wait (a pipeline barrier that did not complete within about one
- * second).  *code = 0 when no kernel reported one.  Synchronizes the device. */
+ * second) or met a bad id (W4A16_DEVERR_*).  *code = 0 when no kernel reported one.
+ * Synchronizes the device. */
 w4a16_status w4a16_device_error(int32_t* code);
 
 /* Human-readable name of a status code (static string, never NULL). */

@@ -9,6 +9,15 @@ the first call raises ImportError if the library is missing.
     packed, scales, zeros = quantize(W, g=128, sym=False)   # W: bf16 [N, K] on cuda
     Y = gemm(X, packed, scales, zeros, g=128, sym=False)      # X: bf16 [M, K] -> Y [M, N]
     W_hat = dequantize(packed, scales, zeros, g=128, sym=False)
+
+Around the linear layer: the gated feed-forward block (``gated``), its backward pass and
+the linear layer's gradients (``gated_backward``, ``gemm_dgrad``, ``gemm_wgrad``), and the
+quantized embedding with its table's gradient (``embedding``, ``embedding_grad``):
+
+    H, G, U = gated(X, gate, up, act="silu", save=True)       # gate, up: quantize(...) triples
+    Y = gemm(H, *down)
+    dH = gemm_dgrad(dY, *down)
+    dX, dG, dU = gated_backward(dH, G, U, gate, up, act="silu")
 """
 from __future__ import annotations
 
@@ -20,6 +29,8 @@ import torch
 
 __all__ = ["lib", "quantize", "dequantize", "gemm", "gemm_decode_noalloc", "plan", "plan8",
            "quantize8", "dequantize8", "gemm8", "quantize_act8", "gemm_w8a8", "linear_w8a8",
+           "gated", "gated8", "gated_backward", "gated8_backward", "gemm_dgrad", "gemm8_dgrad",
+           "gemm_wgrad", "embedding", "embedding8", "embedding_grad",
            "workspace_size", "device_error", "W4A16Error", "PATH_AUTO", "PATH_DECODE", "PATH_TENSORCORE", "STATIC_WEIGHTS", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw4a16.so")
@@ -88,6 +99,28 @@ def _load() -> ctypes.CDLL:
                  "w8a16_gemm", "w8a16_gemm_plan", "w8a16_gemm_ex",
                  "w8a8_quantize_activations", "w8a8_gemm"):
         getattr(lib, name).restype = ctypes.c_int
+    f32 = ctypes.c_float
+    if not hasattr(lib, "w4a16_gated"):
+        raise ImportError(f"{LIB_PATH} is older than this binding: rebuild it")
+    for w in ("w4a16", "w8a16"):
+        for name, args in (
+                ("gated", [vp, i64, i64, *[vp] * 6, i64, i32, i32, i32, *[vp] * 4, sz, i32, vp]),
+                ("gated_backward", [vp, vp, vp, i64, i64, *[vp] * 6, i64, i32, i32, i32, *[vp] * 4,
+                                    sz, vp]),
+                ("gemm_dgrad", [vp, i64, i64, vp, vp, vp, i64, i32, i32, vp, vp, sz, vp]),
+                ("embedding", [vp, i32, i64, vp, vp, vp, i64, i64, i32, i32, f32, vp, vp])):
+            fn = getattr(lib, f"{w}_{name}")
+            fn.argtypes, fn.restype = args, ctypes.c_int
+        fn = getattr(lib, f"{w}_gated_workspace_size")
+        fn.argtypes, fn.restype = [i64, i64, i64, i32, i32], sz
+    lib.w4a16_gemm_wgrad.argtypes = [vp, vp, i64, i64, i64, vp, vp, sz, vp]
+    lib.w4a16_gemm_wgrad.restype = ctypes.c_int
+    lib.w4a16_embedding_grad.argtypes = [vp, vp, i32, i64, i64, i64, f32, i32, vp, vp, sz, vp]
+    lib.w4a16_embedding_grad.restype = ctypes.c_int
+    for name, args in (("gated_backward", [i64, i64, i64, i32]), ("gemm_dgrad", [i64, i64, i64, i32]),
+                       ("gemm_wgrad", [i64, i64]), ("embedding_grad", [i64, i64, i64])):
+        fn = getattr(lib, f"w4a16_{name}_workspace_size")
+        fn.argtypes, fn.restype = args, sz
     if lib.w4a16_abi_version() != ABI_VERSION:
         raise ImportError(f"{LIB_PATH} has ABI version {lib.w4a16_abi_version()}, this binding "
                           f"expects {ABI_VERSION}: rebuild it")
@@ -549,7 +582,306 @@ def linear_w8a8(X: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,
 
 
 def device_error() -> int:
-    """Read and clear the device error word (0 = no kernel gave up a wait)."""
+    """Read and clear the device error word (0: nothing; 1: a kernel gave up a bounded
+    wait; 2: an embedding met an id not below its table's rows)."""
     code = ctypes.c_int32(0)
     _check(lib().w4a16_device_error(ctypes.byref(code)), "w4a16_device_error")
     return int(code.value)
+
+
+# ---------------------------------------------------------------- gated block, gradients, embedding
+_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+
+
+def _act_id(act: str) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return _ACTS[act]
+
+
+def _weights(w, K: int | None, sym: bool, bits: int, name: str = ""):
+    """Checks a (codes, scales, zeros) triple and returns it with its N and K."""
+    codes, scales, zeros = w
+    _need(codes, torch.uint8, f"{name}codes" if bits == 8 else f"{name}packed")
+    _need(scales, torch.bfloat16, f"{name}scales")
+    if not sym:
+        _need(zeros, torch.bfloat16, f"{name}zeros")
+    N, kw = codes.shape[0], codes.shape[1] * (8 // bits)
+    if K is not None and kw != K:
+        raise ValueError(f"{name}weights have K={kw}, the activations have K={K}")
+    _same_device(codes.device, scales=scales, zeros=None if sym else zeros)
+    return codes, scales, None if sym else zeros, N, kw
+
+
+def _groups_ok(scales, zeros, N: int, K: int, g: int, name: str = "") -> None:
+    want = (N, K // g if g > 0 else 0)
+    for what, t in (("scales", scales), ("zeros", zeros)):
+        if t is not None and tuple(t.shape) != want:
+            raise ValueError(f"{name}{what} must be {list(want)} for g={g}, got {list(t.shape)}")
+
+
+def _result(out, shape, dtype, dev, name: str = "out") -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(out, dtype, name, ndim=len(shape))
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(out.shape)}")
+    _same_device(dev, **{name: out})
+    return out
+
+
+def _on(dev: torch.device):
+    return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else _NO_CONTEXT
+
+
+def _scratch(nbytes: int, dev: torch.device):
+    """Workspace of one call, from the caching allocator on the current stream: calls on
+    other streams and captured graphs get memory of their own."""
+    return torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _gated(X, gate, up, g, sym, act, out, save, path, static_weights, bits):
+    _need(X, torch.bfloat16, "X")
+    M, K = X.shape
+    sym = bool(sym)
+    gc, gs, gz, N, _ = _weights(gate, K, sym, bits, "gate ")
+    uc, us, uz, Nu, _ = _weights(up, K, sym, bits, "up ")
+    if Nu != N:
+        raise ValueError(f"gate has {N} rows, up has {Nu}")
+    _groups_ok(gs, gz, N, K, g, "gate ")
+    _groups_ok(us, uz, N, K, g, "up ")
+    dev = gc.device
+    _same_device(dev, X=X, up=uc)
+    aid = _act_id(act)
+    pid = _PATHS[path] if isinstance(path, str) else int(path)
+    with _on(dev):
+        H = _result(out, (M, N), torch.bfloat16, dev)
+        G = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if save else None
+        U = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if save else None
+        L = lib()
+        key = ("gated", bits, dev.index, M, N, K, g, pid)
+        nbytes = _plan_bytes.get(key)
+        if nbytes is None:
+            size = L.w8a16_gated_workspace_size if bits == 8 else L.w4a16_gated_workspace_size
+            nbytes = _plan_bytes[key] = int(size(M, N, K, g, pid))
+        ws = _scratch(nbytes, dev)
+        call = L.w8a16_gated if bits == 8 else L.w4a16_gated
+        _check(call(_p(X), M, K, _p(gc), _p(gs), _p(gz), _p(uc), _p(us), _p(uz), N, g, int(sym), aid,
+                    _p(H), _p(G), _p(U), _p(ws), nbytes,
+                    pid | (STATIC_WEIGHTS if static_weights else 0),
+                    torch.cuda.current_stream(dev).cuda_stream),
+               f"w{bits}a16_gated")
+    return (H, G, U) if save else H
+
+
+def gated(X: torch.Tensor, gate: tuple, up: tuple, g: int = 128, sym: bool = False,
+          act: str = "silu", out: torch.Tensor | None = None, save: bool = False,
+          path: str | int = "auto", static_weights: bool = False):
+    """Gated feed-forward block H[M, N] = act(X·Ŵgateᵀ) ⊙ (X·Ŵupᵀ) with 4-bit weights, in
+    one kernel (bf16 in and out, fp32 accumulation and activation).
+
+    ``gate`` and ``up`` are (packed, scales, zeros) as ``quantize`` returns them (zeros
+    may be None when ``sym``); ``act`` is "silu", "gelu", "gelu_tanh" or "relu".
+    ``save`` returns (H, G, U) with the two projections, as ``gated_backward`` takes
+    them.  ``path`` and ``static_weights`` as in ``gemm``."""
+    return _gated(X, gate, up, g, sym, act, out, save, path, static_weights, 4)
+
+
+def gated8(X: torch.Tensor, gate: tuple, up: tuple, g: int = 128, sym: bool = False,
+           act: str = "silu", out: torch.Tensor | None = None, save: bool = False,
+           path: str | int = "auto", static_weights: bool = False):
+    """``gated`` with 8-bit codes (weights from ``quantize8``)."""
+    return _gated(X, gate, up, g, sym, act, out, save, path, static_weights, 8)
+
+
+def _gated_backward(dH, G, U, gate, up, g, sym, act, out, bits):
+    for name, t in (("dH", dH), ("G", G), ("U", U)):
+        _need(t, torch.bfloat16, name)
+    M, N = dH.shape
+    if tuple(G.shape) != (M, N) or tuple(U.shape) != (M, N):
+        raise ValueError("dH, G and U must have one shape")
+    sym = bool(sym)
+    gc, gs, gz, Nw, K = _weights(gate, None, sym, bits, "gate ")
+    uc, us, uz, Nu, _ = _weights(up, K, sym, bits, "up ")
+    if Nw != N or Nu != N:
+        raise ValueError(f"dH has {N} columns, gate has {Nw} rows, up has {Nu}")
+    _groups_ok(gs, gz, N, K, g, "gate ")
+    _groups_ok(us, uz, N, K, g, "up ")
+    dev = gc.device
+    _same_device(dev, dH=dH, G=G, U=U, up=uc)
+    aid = _act_id(act)
+    with _on(dev):
+        dX = _result(out, (M, K), torch.bfloat16, dev)
+        dG = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        dU = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        L = lib()
+        nbytes = int(L.w4a16_gated_backward_workspace_size(M, N, K, g))
+        ws = _scratch(nbytes, dev)
+        call = L.w8a16_gated_backward if bits == 8 else L.w4a16_gated_backward
+        _check(call(_p(dH), _p(G), _p(U), M, N, _p(gc), _p(gs), _p(gz), _p(uc), _p(us), _p(uz), K, g,
+                    int(sym), aid, _p(dX), _p(dG), _p(dU), _p(ws), nbytes,
+                    torch.cuda.current_stream(dev).cuda_stream),
+               f"w{bits}a16_gated_backward")
+    return dX, dG, dU
+
+
+def gated_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, gate: tuple, up: tuple,
+                   g: int = 128, sym: bool = False, act: str = "silu",
+                   out: torch.Tensor | None = None):
+    """Backward pass of ``gated``: (dX, dG, dU) for the gradient dH[M, N] of H and the
+    projections G and U that ``gated(..., save=True)`` returned.
+
+    dG = dH·U·act'(G) and dU = dH·act(G) are the gradients at the projections' outputs
+    (``gemm_wgrad(dG, X)`` is the gate weight's straight-through gradient);
+    dX[M, K] = dG·Ŵgate + dU·Ŵup (``out`` when given)."""
+    return _gated_backward(dH, G, U, gate, up, g, sym, act, out, 4)
+
+
+def gated8_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, gate: tuple, up: tuple,
+                    g: int = 128, sym: bool = False, act: str = "silu",
+                    out: torch.Tensor | None = None):
+    """``gated_backward`` with 8-bit codes."""
+    return _gated_backward(dH, G, U, gate, up, g, sym, act, out, 8)
+
+
+def _dgrad(dY, w, g, sym, out, bits):
+    _need(dY, torch.bfloat16, "dY")
+    M, N = dY.shape
+    sym = bool(sym)
+    codes, scales, zeros, Nw, K = _weights(w, None, sym, bits)
+    if Nw != N:
+        raise ValueError(f"dY has {N} columns, the weights have {Nw} rows")
+    _groups_ok(scales, zeros, N, K, g)
+    dev = codes.device
+    _same_device(dev, dY=dY)
+    with _on(dev):
+        dX = _result(out, (M, K), torch.bfloat16, dev)
+        L = lib()
+        nbytes = int(L.w4a16_gemm_dgrad_workspace_size(M, N, K, g))
+        ws = _scratch(nbytes, dev)
+        call = L.w8a16_gemm_dgrad if bits == 8 else L.w4a16_gemm_dgrad
+        _check(call(_p(dY), M, N, _p(codes), _p(scales), _p(zeros), K, g, int(sym), _p(dX), _p(ws), nbytes,
+                    torch.cuda.current_stream(dev).cuda_stream),
+               f"w{bits}a16_gemm_dgrad")
+    return dX
+
+
+def gemm_dgrad(dY: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+               zeros: torch.Tensor | None, g: int = 128, sym: bool = False,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of ``gemm`` with respect to X: dX[M, K] = dY[M, N]·Ŵ[N, K], read from the
+    packed codes as they are (nothing is transposed or expanded in memory)."""
+    return _dgrad(dY, (packed, scales, zeros), g, sym, out, 4)
+
+
+def gemm8_dgrad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+                zeros: torch.Tensor | None, g: int = 128, sym: bool = False,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """``gemm_dgrad`` with 8-bit codes."""
+    return _dgrad(dY, (codes, scales, zeros), g, sym, out, 8)
+
+
+def gemm_wgrad(dY: torch.Tensor, X: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of a linear layer with respect to its dense weight: dW[N, K] =
+    dY[M, N]ᵀ·X[M, K] (bf16, fp32 accumulation).  With weights quantized anew in every
+    step it is the straight-through gradient of the weight that was quantized."""
+    _need(dY, torch.bfloat16, "dY")
+    _need(X, torch.bfloat16, "X")
+    M, N = dY.shape
+    K = X.shape[1]
+    if X.shape[0] != M:
+        raise ValueError(f"dY has {M} rows, X has {X.shape[0]}")
+    dev = X.device
+    if dY.device != dev:
+        raise ValueError(f"dY is on {dY.device}, X is on {dev}")
+    with _on(dev):
+        dW = _result(out, (N, K), torch.bfloat16, dev)
+        L = lib()
+        nbytes = int(L.w4a16_gemm_wgrad_workspace_size(M, N))
+        ws = _scratch(nbytes, dev)
+        _check(L.w4a16_gemm_wgrad(_p(dY), _p(X), M, N, K, _p(dW), _p(ws), nbytes,
+                                  torch.cuda.current_stream(dev).cuda_stream), "w4a16_gemm_wgrad")
+    return dW
+
+
+def _need_ids(ids: torch.Tensor) -> int:
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
+    if not ids.is_cuda:
+        raise ValueError("ids must be on a CUDA device")
+    if not ids.is_contiguous():
+        raise ValueError("ids must be contiguous")
+    return ids.element_size()
+
+
+def _embedding(ids, w, g, sym, scale, out, bits):
+    id_bytes = _need_ids(ids)
+    sym = bool(sym)
+    codes, scales, zeros, V, K = _weights(w, None, sym, bits)
+    _groups_ok(scales, zeros, V, K, g)
+    dev = codes.device
+    _same_device(dev, ids=ids)
+    with _on(dev):
+        Y = _result(out, (*ids.shape, K), torch.bfloat16, dev)
+        L = lib()
+        call = L.w8a16_embedding if bits == 8 else L.w4a16_embedding
+        _check(call(_p(ids), id_bytes, ids.numel(), _p(codes), _p(scales), _p(zeros), V, K, g, int(sym),
+                    float(scale), _p(Y), torch.cuda.current_stream(dev).cuda_stream),
+               f"w{bits}a16_embedding")
+    return Y
+
+
+def embedding(ids: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
+              zeros: torch.Tensor | None, g: int = 128, sym: bool = False, scale: float = 1.0,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows of a 4-bit table [V, K]: out[..., :] = bf16(scale·Ŵ[ids, :]).
+
+    ``ids`` is an int32 or int64 tensor of any shape.  An id below 0 is padding: its row
+    is zeros.  An id not below V gives zeros as well and is reported by
+    ``device_error()`` (2)."""
+    return _embedding(ids, (packed, scales, zeros), g, sym, scale, out, 4)
+
+
+def embedding8(ids: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
+               zeros: torch.Tensor | None, g: int = 128, sym: bool = False, scale: float = 1.0,
+               out: torch.Tensor | None = None) -> torch.Tensor:
+    """``embedding`` from an 8-bit table."""
+    return _embedding(ids, (codes, scales, zeros), g, sym, scale, out, 8)
+
+
+def embedding_grad(dY: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1.0,
+                   dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of the dense table behind ``embedding``: dW[V, K] with
+    dW[v, :] = scale·Σ_{ids = v} dY[..., :], in fp32 over the tokens sorted by id (the
+    same inputs give the same bits), zeros for rows no token names.
+
+    dY is bf16 [*ids.shape, K]; ``dtype`` float32 or bfloat16.  Ids below 0 (padding) and
+    not below V add nothing; the latter are reported by ``device_error()`` (2)."""
+    id_bytes = _need_ids(ids)
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+    _need(dY, torch.bfloat16, "dY", ndim=ids.dim() + 1)
+    if tuple(dY.shape[:-1]) != tuple(ids.shape):
+        raise ValueError(f"dY has shape {list(dY.shape)}, ids {list(ids.shape)}")
+    dev = dY.device
+    if ids.device != dev:
+        raise ValueError(f"ids is on {ids.device}, dY is on {dev}")
+    V, K, T = int(V), dY.shape[-1], ids.numel()
+    if V < 0:
+        raise ValueError(f"V must not be negative, got {V}")
+    with _on(dev):
+        dW = _result(out, (V, K), dtype, dev)
+        L = lib()
+        nbytes = int(L.w4a16_embedding_grad_workspace_size(T, V, K))
+        ws = _scratch(nbytes, dev)
+        _check(L.w4a16_embedding_grad(_p(dY), _p(ids), id_bytes, T, V, K, float(scale),
+                                      int(dtype == torch.float32), _p(dW), _p(ws), nbytes,
+                                      torch.cuda.current_stream(dev).cuda_stream),
+               "w4a16_embedding_grad")
+    return dW

@@ -1,0 +1,53 @@
+// Activations of the gated feed-forward block, in binary32.
+//
+//   silu       x·p, p = 1/(1 + e^−x)                    derivative p·(1 + x·(1 − p))
+//   gelu       x·Φ(x), Φ(x) = (1 + erf(x/√2))/2          Φ(x) + x·φ(x)
+//   gelu_tanh  x/2·(1 + t), t = tanh(c·(x + a·x³))       (1 + t)/2 + x/2·(1 − t²)·c·(1 + 3a·x²)
+//              with c = √(2/π), a = 0.044715
+//   relu       max(x, 0)                                  1 for x > 0, else 0
+// A NaN stays a NaN.  The results are rounded to bf16 after one more product, so the
+// relative error of the approximate exponential (about 2^-21) is far below that rounding.
+#pragma once
+
+#include "../../include/w4a16.h"
+
+namespace w4a16 {
+
+__device__ __forceinline__ float sigmoid_f32(float x) {
+    return __fdividef(1.0f, 1.0f + __expf(-x));     // e^−x = inf gives 0, e^−x = 0 gives 1
+}
+
+__device__ __forceinline__ float tanh_arg(float x) {
+    return 0.7978845608028654f * (x + 0.044715f * x * x * x);
+}
+
+__device__ __forceinline__ float act_value(int kind, float x) {
+    if (kind == W4A16_ACT_SILU) return x * sigmoid_f32(x);
+    if (kind == W4A16_ACT_GELU) return 0.5f * x * erfcf(-0.7071067811865476f * x);
+    // (1 + tanh y)/2 = sigmoid(2y)
+    if (kind == W4A16_ACT_GELU_TANH) return x * sigmoid_f32(2.0f * tanh_arg(x));
+    return x != x ? x : fmaxf(x, 0.0f);
+}
+
+// The activation and its derivative.
+__device__ __forceinline__ void act_value_grad(int kind, float x, float& a, float& d) {
+    if (kind == W4A16_ACT_SILU) {
+        const float p = sigmoid_f32(x);
+        a = x * p;
+        d = p * (1.0f + x * (1.0f - p));
+    } else if (kind == W4A16_ACT_GELU) {
+        const float c = 0.5f * erfcf(-0.7071067811865476f * x);
+        a = x * c;
+        d = c + x * (0.3989422804014327f * __expf(-0.5f * x * x));
+    } else if (kind == W4A16_ACT_GELU_TANH) {
+        const float c = sigmoid_f32(2.0f * tanh_arg(x));          // (1 + t)/2
+        a = x * c;
+        // (1 − t²)/2 = 2·c·(1 − c)
+        d = c + x * (2.0f * c * (1.0f - c)) * (0.7978845608028654f * (1.0f + 0.134145f * x * x));
+    } else {
+        a = x != x ? x : fmaxf(x, 0.0f);
+        d = x > 0.0f ? 1.0f : 0.0f;
+    }
+}
+
+}  // namespace w4a16

@@ -61,8 +61,16 @@
 //  * Programmatic dependent launch lets the next kernel on the stream start
 //    while this one drains; nothing but those static weights is read, and
 //    nothing is written, before griddepcontrol.wait.
+//  * GATED (the gated feed-forward block, H = act(X·Ŵgᵀ) ⊙ (X·Ŵuᵀ)): a unit is 128 rows
+//    of the gate projection and the same 128 rows of the up projection (two TMA boxes
+//    of 16 KB), and warp w owns 8 of each: rows 0..7 of its MMA tile are gate rows,
+//    rows 8..15 the same features' up rows.  An accumulator fragment holds rows g and
+//    g + 8 of the tile, so each lane ends with G and U of the same feature and tokens
+//    and forms act(G)·U in registers, from binary32 sums: no exchange, and nothing but
+//    H (and G and U when they are kept) is written.
 #pragma once
 
+#include "activation.cuh"
 #include "common.cuh"
 
 namespace w4a16 {
@@ -145,10 +153,25 @@ struct UnitWalk {
     }
 };
 
+// Tensor maps of a launch (GATED: P, S, Z of the gate projection, P2, S2, Z2 of the up one).
+template <bool GATED>
+struct DecodeMaps {
+    CUtensorMap P, X, S, Z;
+};
+template <>
+struct DecodeMaps<true> {
+    CUtensorMap P, X, S, Z, P2, S2, Z2;
+};
+
 struct DecodeArgs {
     const uint16_t* scales;
     const uint16_t* zeros;
-    uint16_t* Y;
+    const uint16_t* scales2;     // GATED: the up projection's
+    const uint16_t* zeros2;
+    uint16_t* Y;                 // GATED: H
+    uint16_t* G;                 // GATED: the projections' outputs, or null
+    uint16_t* U;
+    int act;                     // GATED: w4a16_act
     const uint16_t* act_scale;   // bf16 [K] per-input-channel activation scale, or null
     uint32_t* ws_flag;    // [(RB + C) slots][16 warps] ready flags
     float* ws_part;       // [(RB + C) slots][16 warps][32 lanes][4·MB] fp32 parts
@@ -168,7 +191,7 @@ struct DecodeArgs {
     int sz_copy;          // without TMA: bytes per scale copy, 16, 8 or 4 (cp.async), 2 (plain);
                           // 3: one group per unit, copied as the 4-byte aligned pair holding it
     int early;            // 1: the previous grid does not write the weights; stream them before the dependency wait
-    int64_t U;            // units = RB · KBn
+    int64_t units;        // RB · KBn
 };
 
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes) {
@@ -245,18 +268,31 @@ __device__ __forceinline__ bool wait_flag(const uint32_t* flag) {
     }
 }
 
+// Output feature of row r of a unit of row block rb, and the scale (arr 0) or zero
+// (arr 1) array that holds its groups.
+template <bool GATED>
+__device__ __forceinline__ int unit_feature(int rb, int r) {
+    return GATED ? rb * (kDecRows / 2) + (r & (kDecRows / 2 - 1)) : rb * kDecRows + r;
+}
+
+template <bool GATED>
+__device__ __forceinline__ const uint16_t* scale_base(const DecodeArgs& a, int arr, int r) {
+    if (GATED && r >= kDecRows / 2) return arr == 0 ? a.scales2 : a.zeros2;
+    return arr == 0 ? a.scales : a.zeros;
+}
+
 // The producer's cp.async copies of a unit's scales (and zeros) when their rows
 // are not 16-byte aligned: per array and row, GU·2 bytes as copies of CS bytes,
 // lane l taking rows l, l + 32, ... (no integer division in the loop).
-template <int GU, int CS>
+template <int GU, int CS, bool GATED>
 __device__ __forceinline__ void copy_scale_rows(const DecodeArgs& a, uint32_t sz, int sz_array, int rb,
                                                 int g0, int arrays, int lane) {
     constexpr int kPerRow = (GU * 2 + CS - 1) / CS;
     for (int arr = 0; arr < arrays; ++arr) {
-        const uint16_t* base = arr == 0 ? a.scales : a.zeros;
 #pragma unroll 1
         for (int r = lane; r < kDecRows; r += 32) {
-            const int n = rb * kDecRows + r;
+            const uint16_t* base = scale_base<GATED>(a, arr, r);
+            const int n = unit_feature<GATED>(rb, r);
             const uint32_t dst = sz + arr * sz_array + r * GU * 2;
 #pragma unroll
             for (int t = 0; t < kPerRow; ++t) {
@@ -287,6 +323,29 @@ __device__ __forceinline__ void decode_store_y(const DecodeArgs& a, const float 
         }
 }
 
+// GATED: lane (g, q) holds G of feature 8w + g in d[mb][0..1] and U in d[mb][2..3], for
+// tokens 8mb + 2q and + 1.  H is rounded once, from the binary32 sums; G and U, when
+// they are kept for a backward pass, are rounded apart.
+template <int MB>
+__device__ __forceinline__ void decode_store_gated(const DecodeArgs& a, const float (&d)[MB][4], int rb,
+                                                   int w, int g, int q) {
+    const int n = rb * (kDecRows / 2) + 8 * w + g;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int m = 8 * mb + 2 * q + j;
+            if (m < a.M && n < a.N) {
+                const int64_t at = (int64_t)m * a.N + n;
+                a.Y[at] = (uint16_t)f32_to_bf16_bits_rn(act_value(a.act, d[mb][j]) * d[mb][2 + j]);
+                if (a.G != nullptr) {
+                    a.G[at] = (uint16_t)f32_to_bf16_bits_rn(d[mb][j]);
+                    a.U[at] = (uint16_t)f32_to_bf16_bits_rn(d[mb][2 + j]);
+                }
+            }
+        }
+}
+
 // Four 8-bit codes of a word -> (q0, q1) and (q2, q3) as bf16 pairs of
 // bf16_rn((q − z)·s).  The byte placed in a binary32 mantissa gives 2^23 + q
 // exactly; subtracting zoff = 2^23 + z leaves q − z (exact), the product with s
@@ -302,12 +361,10 @@ __device__ __forceinline__ void dq_word8(uint32_t w, float s, float zoff, uint32
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(f[3]), "f"(f[2]));
 }
 
-template <int MB, bool SYM, int G, int BITS>
+template <int MB, bool SYM, int G, int BITS, bool GATED = false>
 __global__ void __launch_bounds__(kDecThreads, 1)
-    gemv_decode_kernel(const __grid_constant__ CUtensorMap tmP,
-                       const __grid_constant__ CUtensorMap tmX,
-                       const __grid_constant__ CUtensorMap tmS,
-                       const __grid_constant__ CUtensorMap tmZ, const DecodeArgs a) {
+    gemv_decode_kernel(const __grid_constant__ DecodeMaps<GATED> maps, const DecodeArgs a) {
+    constexpr int kBoxRows = GATED ? kDecRows / 2 : kDecRows;   // rows per TMA box
     // G == 0: per-channel granularity, one scale (and zero) per row for all of K.
     constexpr int BK = dec_block_k<BITS>();            // K per unit
     constexpr int XRB = dec_x_row_bytes<BITS>();
@@ -340,8 +397,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const int lane = threadIdx.x & 31;
     const int64_t C = gridDim.x;
     const int64_t cta = blockIdx.x;
-    const int64_t u0 = cta * a.U / C;
-    const int64_t u1 = (cta + 1) * a.U / C;
+    const int64_t u0 = cta * a.units / C;
+    const int64_t u1 = (cta + 1) * a.units / C;
     const int nunits = (int)(u1 - u0);
     const int M = a.M;
 
@@ -368,11 +425,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     if (warp == kDecProducerWarp) {
         // ---------------------------------------------------------------- producer
         if (lane == 0) {
-            prefetch_tensormap(&tmP);
-            prefetch_tensormap(&tmX);
+            prefetch_tensormap(&maps.P);
+            prefetch_tensormap(&maps.X);
             if (a.sz_tma) {
-                prefetch_tensormap(&tmS);
-                if (!SYM) prefetch_tensormap(&tmZ);
+                prefetch_tensormap(&maps.S);
+                if (!SYM) prefetch_tensormap(&maps.Z);
+            }
+            if constexpr (GATED) {
+                prefetch_tensormap(&maps.P2);
+                if (a.sz_tma) {
+                    prefetch_tensormap(&maps.S2);
+                    if (!SYM) prefetch_tensormap(&maps.Z2);
+                }
             }
         }
         const uint32_t tx = (uint32_t)kDecPBytes + (uint32_t)M * XRB;
@@ -400,8 +464,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 const uint32_t sb = smem_u32(&sfull[slab_slot]);
                 const uint32_t dst = smem_u32(slab_base + slab_slot * kDecSlabBytes);
                 mbar_arrive_expect_tx(sb, (uint32_t)((SYM ? 1 : 2) * kDecSlabArrayBytes));
-                tma_load_2d(dst, &tmS, 8 * j, rb * kDecRows, sb);
-                if (!SYM) tma_load_2d(dst + kDecSlabArrayBytes, &tmZ, 8 * j, rb * kDecRows, sb);
+                tma_load_2d(dst, &maps.S, 8 * j, rb * kBoxRows, sb);
+                if (!SYM) tma_load_2d(dst + kDecSlabArrayBytes, &maps.Z, 8 * j, rb * kBoxRows, sb);
+                if constexpr (GATED) {
+                    const uint32_t d2 = dst + kDecSlabArrayBytes / 2;
+                    tma_load_2d(d2, &maps.S2, 8 * j, rb * kBoxRows, sb);
+                    if (!SYM) tma_load_2d(d2 + kDecSlabArrayBytes, &maps.Z2, 8 * j, rb * kBoxRows, sb);
+                }
             }
             slab_rb = rb;
             slab_j = j;
@@ -415,7 +484,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             const uint32_t bar = smem_u32(&full[s]);
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar, tx);
-                tma_load_2d(st, &tmP, kb * kDecUnitRowBytes, rb * kDecRows, bar);
+                tma_load_2d(st, &maps.P, kb * kDecUnitRowBytes, rb * kBoxRows, bar);
+                if constexpr (GATED)
+                    tma_load_2d(st + kDecPBytes / 2, &maps.P2, kb * kDecUnitRowBytes, rb * kBoxRows, bar);
             }
             const uint32_t sz = st + (uint32_t)a.sz_off;
             if (G != 0 && a.sz_tma) {
@@ -424,9 +495,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 // per-channel: the row block's contiguous, 16-byte aligned scales (and zeros)
                 for (int e = lane; e < (kDecRows / 8) * arrays; e += 32) {
                     const int arr = e / (kDecRows / 8), j = e % (kDecRows / 8);
-                    const int n = rb * kDecRows + 8 * j;
+                    const int n = unit_feature<GATED>(rb, 8 * j);
                     const int valid = min(max(a.N - n, 0), 8);
-                    const uint16_t* src = (arr == 0 ? a.scales : a.zeros) + (valid > 0 ? n : 0);
+                    const uint16_t* src = scale_base<GATED>(a, arr, 8 * j) + (valid > 0 ? n : 0);
                     cp_async_16(sz + arr * kSzArray + 16 * j, src, 2u * (uint32_t)valid);
                 }
                 cp_async_arrive_noinc(bar);
@@ -438,12 +509,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     // of cs, so a copy never straddles the end of a scale row
                     // (the host picks cs ≤ GU·2; instances with larger copies are never built)
                     if constexpr (GU * 2 >= 16) {
-                        if (cs == 16) copy_scale_rows<GU, 16>(a, sz, kSzArray, rb, g0, arrays, lane);
+                        if (cs == 16) copy_scale_rows<GU, 16, GATED>(a, sz, kSzArray, rb, g0, arrays, lane);
                     }
                     if constexpr (GU * 2 >= 8) {
-                        if (cs == 8) copy_scale_rows<GU, 8>(a, sz, kSzArray, rb, g0, arrays, lane);
+                        if (cs == 8) copy_scale_rows<GU, 8, GATED>(a, sz, kSzArray, rb, g0, arrays, lane);
                     }
-                    if (cs == 4) copy_scale_rows<GU, 4>(a, sz, kSzArray, rb, g0, arrays, lane);
+                    if (cs == 4) copy_scale_rows<GU, 4, GATED>(a, sz, kSzArray, rb, g0, arrays, lane);
                     cp_async_arrive_noinc(bar);
                 } else if (cs == 3) {
                     // one group per unit (8-bit codes at g = 128) and an even number of
@@ -452,10 +523,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     if constexpr (GU == 1) {
                         const int gp = g0 & ~1;
                         for (int arr = 0; arr < arrays; ++arr) {
-                            const uint16_t* base = arr == 0 ? a.scales : a.zeros;
 #pragma unroll 4
                             for (int r = lane; r < kDecRows; r += 32) {
-                                const int n = rb * kDecRows + r;
+                                const uint16_t* base = scale_base<GATED>(a, arr, r);
+                                const int n = unit_feature<GATED>(rb, r);
                                 const bool in = n < a.N && gp < a.Gtot;
                                 cp_async_4(sz + arr * kSzArray + r * 4, base + (in ? (int64_t)n * a.Gtot + gp : 0),
                                            in ? 4u : 0u);
@@ -477,8 +548,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                                 const int arr = e / (kDecRows * GU);
                                 const int rem = e - arr * (kDecRows * GU);
                                 const int r = rem / GU, j = rem - r * GU;
-                                const int n = rb * kDecRows + r;
-                                const uint16_t* src = arr == 0 ? a.scales : a.zeros;
+                                const int n = unit_feature<GATED>(rb, r);
+                                const uint16_t* src = scale_base<GATED>(a, arr, r);
                                 if (n < a.N && g0 + j < a.Gtot) v[t] = ldg_u16(src + (int64_t)n * a.Gtot + g0 + j);
                             }
                         }
@@ -501,7 +572,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         };
         auto load_x = [&](int kb, int s) {
             if (lane == 0)
-                tma_load_2d(stages_u32 + (uint32_t)(s * a.stage_bytes) + kDecPBytes, &tmX, kb * BK, 0,
+                tma_load_2d(stages_u32 + (uint32_t)(s * a.stage_bytes) + kDecPBytes, &maps.X, kb * BK, 0,
                             smem_u32(&full[s]));
         };
 
@@ -639,8 +710,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const int q = lane & 3;
     // Codes of rows r0 = 16w + g and r0 + 8 (1024 bytes further), chunk 2q + h:
     // the 128-byte swizzle puts logical chunk c of row r at chunk c ^ (r % 8).
-    const uint32_t a_off0 = (uint32_t)((16 * w + g) * 128 + (((2 * q) ^ g) * 16));
-    const uint32_t a_off1 = (uint32_t)((16 * w + g) * 128 + (((2 * q + 1) ^ g) * 16));
+    // GATED: rows 8w + g of the gate tile and of the up tile (16 KB further).
+    constexpr int kWarpRows = GATED ? 8 : 16;
+    constexpr int kRow8 = GATED ? kDecRows / 2 : 8;          // the lane's second row, from its first
+    const uint32_t a_off0 = (uint32_t)((kWarpRows * w + g) * 128 + (((2 * q) ^ g) * 16));
+    const uint32_t a_off1 = (uint32_t)((kWarpRows * w + g) * 128 + (((2 * q + 1) ^ g) * 16));
     // This lane's B fragments: fragment-ordered X row g (and g + 8), or zeros for
     // columns beyond M.
     const bool col0 = g < M;
@@ -654,8 +728,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     constexpr int kG = G == 0 ? 1 : G;
     const int sgrp0 = G == 0 ? 0 : ((BITS == 4 ? 64 : 32) * q) / kG;
     const int sgrp1 = G == 0 ? 0 : ((BITS == 4 ? 64 : 32) * q + (BITS == 4 ? 32 : 16)) / kG;
-    const int srow0 = (16 * w + g) * SW * 2;         // within the stage's scale area or a slab
-    const int srow8 = 8 * SW * 2;                     // row r0 + 8
+    const int srow0 = (kWarpRows * w + g) * SW * 2;  // within the stage's scale area or a slab
+    const int srow8 = kRow8 * SW * 2;                 // row r0 + 8 (GATED: the up row)
     const bool tma_slab = G != 0 && a.sz_tma;
     int slab_rb = -1, slab_j = -1;                   // the slab the consumers read
     int slab_slot = -1;                              // its slot (-1: none yet)
@@ -758,7 +832,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 for (int h = 0; h < 2; ++h) {
                     const uint8_t* ap = stp + (h == 0 ? a_off0 : a_off1);
                     const uint4 va = *reinterpret_cast<const uint4*>(ap);
-                    const uint4 vb = *reinterpret_cast<const uint4*>(ap + 1024);
+                    const uint4 vb = *reinterpret_cast<const uint4*>(ap + 128 * kRow8);
                     const uint32_t w0[4] = {va.x, va.y, va.z, va.w};
                     const uint32_t w1[4] = {vb.x, vb.y, vb.z, vb.w};
                     uint4 xv0[4], xv1[4];
@@ -804,7 +878,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     for (int h = 0; h < 2; ++h) {
                         const uint8_t* ap = stp + (h == 0 ? a_off0 : a_off1);
                         const uint4 va = *reinterpret_cast<const uint4*>(ap);
-                        const uint4 vb = *reinterpret_cast<const uint4*>(ap + 1024);
+                        const uint4 vb = *reinterpret_cast<const uint4*>(ap + 128 * kRow8);
                         const uint32_t w0[4] = {va.x ^ flip, va.y ^ flip, va.z ^ flip, va.w ^ flip};
                         const uint32_t w1[4] = {vb.x ^ flip, vb.y ^ flip, vb.z ^ flip, vb.w ^ flip};
                         // X of this lane's chunk: 16 values at slots 2h, 2h + 1
@@ -859,11 +933,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const int64_t first_u = (int64_t)rb * a.KBn;
         const bool whole = first_u >= u0 && first_u + a.KBn <= u1;
         if (whole) {
-            decode_store_y<MB>(a, d, rb, w, g, q);
+            if constexpr (GATED) decode_store_gated<MB>(a, d, rb, w, g, q);
+            else decode_store_y<MB>(a, d, rb, w, g, q);
             continue;
         }
-        const int64_t c_first = owner_of(first_u, a.U, C);
-        const int64_t c_last = owner_of(first_u + a.KBn - 1, a.U, C);
+        const int64_t c_first = owner_of(first_u, a.units, C);
+        const int64_t c_last = owner_of(first_u + a.KBn - 1, a.units, C);
         if (cta != c_first) {
             // publish this CTA's part, then its ready flag
             const int64_t slot = rb + cta;
@@ -912,7 +987,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (lane == 0)                                        // consumed: the slots are free again
             for (int64_t p = c_first + 1; p <= c_last; ++p)
                 st_relaxed_u32(a.ws_flag + (rb + p) * kDecConsumers + w, 0u);
-        decode_store_y<MB>(a, d, rb, w, g, q);
+        if constexpr (GATED) decode_store_gated<MB>(a, d, rb, w, g, q);
+        else decode_store_y<MB>(a, d, rb, w, g, q);
     }
 }
 

@@ -248,15 +248,21 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parit
 }
 
 // Wait for the phase with the given parity to complete; give up after about a
-// second, record the error and return false.
+// second, record the error and return false.  The global timer is read only once a
+// wait has lasted many tries: a read of it costs more than most waits of a pipeline.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
+    uint64_t t0 = 0;
+    for (uint32_t tries = 1;; ++tries) {
         if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-        if (global_timer_ns() - t0 > kWaitTimeoutNs) {
-            report_error(kErrMbarTimeout);
-            return false;
+        if ((tries & 63u) == 0u) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) {
+                t0 = now;
+            } else if (now - t0 > kWaitTimeoutNs) {
+                report_error(kErrMbarTimeout);
+                return false;
+            }
         }
     }
 }

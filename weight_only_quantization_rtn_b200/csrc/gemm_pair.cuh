@@ -14,19 +14,31 @@
 // 128 x 256 tile with one accumulator uses up (loads, dequantized stores and operand
 // reads together), has room left.
 //
-// PAIR: two CTAs of a cluster compute one tile together (cta_group::2): each holds its
-// own 128 rows of both A tiles and half of the tokens, one thread of the even CTA issues
-// the MMAs (M = 256) for both, and each SM reads half of the B operand.
+// PAIR (more than 128 tokens): two CTAs of a cluster compute one tile together
+// (cta_group::2): each holds its own 128 rows of both A tiles and half of the tokens, one
+// thread of the even CTA issues the MMAs (M = 256) for both, and each SM reads half of
+// the B operand.  The token tile is the batch divided evenly (at most 256 tokens), in
+// steps of 16, not a power of two: 333 tokens are two tiles of 176.
 //
 // DGRAD needs Ŵ with the reduction along its rows.  The codes stay as they are stored:
 // a block is 64 weight rows x 256 input channels, dequantized into the "MN-major" layout
 // (64 channels contiguous per 128-byte swizzled line, lines along the rows), which the
 // tensor core reads as the transposed A operand; nothing is transposed in memory.
 //
-// Warps: 0 loads (TMA: token tile with the 128-byte swizzle, codes), 1 issues the MMAs
-// and owns the tensor memory, 2..9 dequantize and afterwards run the epilogue.  Scales
-// and zero points go from global memory to registers, ahead of their block, so any
-// number of groups per row and any alignment is read the same way.
+// Warps: 0 loads tokens (TMA, 128-byte swizzle), 18 loads codes (TMA), 1 issues the MMAs
+// and owns the tensor memory, 2..17 dequantize and run the epilogue.  Three rings of
+// shared memory, because the three have different sizes and lead times: token blocks,
+// code units (GATED with 4 bits: 128 input channels, so that a row is 64 bytes; loaded as
+// 32-byte rows the TMA engine's row rate, not bandwidth, paced the kernel) and dequantized
+// A tiles.  Each dequantizing thread holds the next block's codes in registers while it
+// works on the current one.  Scales and zero points go from global memory to registers
+// ahead of their block, so any number of groups per row and any alignment is read the
+// same way.
+//
+// The kernel is persistent, one CTA (or pair) per SM (or two): whole tiles are dealt in
+// turn, and what is left (or everything, when there are fewer tiles than CTAs) may be
+// split evenly along the reduction; then each CTA leaves binary32 parts of at most two
+// tiles, which pair_reduce_kernel adds in a fixed order.
 #pragma once
 
 #include "activation.cuh"
@@ -54,14 +66,14 @@ __device__ __forceinline__ uint32_t mapa_u32(uint32_t addr, uint32_t rank) {
 }
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -71,13 +83,17 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 
 // mbar_wait for a barrier that the other CTA of the pair arrives on (bounded).
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    while (true) {
+    uint64_t t0 = 0;
+    for (uint32_t tries = 1;; ++tries) {
         if (mbar_try_wait_cluster(bar, parity)) return true;
-        if (global_timer_ns() - t0 > kWaitTimeoutNs) {
-            report_error(kErrMbarTimeout);
-            return false;
+        if ((tries & 63u) == 0u) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) {
+                t0 = now;
+            } else if (now - t0 > kWaitTimeoutNs) {
+                report_error(kErrMbarTimeout);
+                return false;
+            }
         }
     }
 }
@@ -149,33 +165,27 @@ constexpr uint32_t kIdescAMnMajor = 1u << 15;
 constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
 // ------------------------------------------------------------------ configuration
-constexpr int kPairDequantWarps = 8;
-constexpr int kPairThreads = (2 + kPairDequantWarps) * 32;
-constexpr int kPairBlock = 64;          // reduction per stage
+constexpr int kPairDequantWarps = 16;
+constexpr int kPairCodeWarp = 2 + kPairDequantWarps;
+constexpr int kPairThreads = (kPairCodeWarp + 1) * 32;
+constexpr int kPairBlock = 64;          // reduction per block
 constexpr int kPairRows = 128;          // rows of one A tile per CTA
-constexpr int kPairABytes = 2 * kPairRows * kPairBlock * 2;   // both A tiles of a stage
+constexpr int kPairABytes = 2 * kPairRows * kPairBlock * 2;   // both A tiles of a block: 32 KB
+constexpr int kPairABufs = 3;
+constexpr int kPairStageBytes = kPairDequantWarps * 1024;     // epilogue staging, 1 KB per warp
+constexpr int kPairXBytes = 64 * 1024;                        // token ring
+constexpr int kPairPBytes = 48 * 1024;                        // code ring
+constexpr int kPairMaxX = 8;
+constexpr int kPairSmemBytes = kPairABufs * kPairABytes + kPairXBytes + kPairPBytes + kPairStageBytes + 1024 + 1024;
+static_assert(kPairSmemBytes <= 232448, "shared memory");
 
-// BT: tokens of the CTA's B tile (PAIR: of each CTA; the MMA's N is 2·BT).
-template <int BT, bool PAIR, int BITS>
-struct PairConfig {
-    static constexpr int kMmaN = PAIR ? 2 * BT : BT;
-    static constexpr int kXBytes = BT * kPairBlock * 2;
-    static constexpr int kPBytes = 2 * kPairRows * kPairBlock * BITS / 8;   // codes of a stage
-    // Small token tiles: the loads of a stage are small beside the A tiles they turn into,
-    // and they come from HBM, so they get a ring of their own, deep enough to cover the
-    // memory latency; large tiles keep one ring (slot i holds X, codes and A tiles).
-    static constexpr bool kSplitRing = !PAIR && BT < 128;
-    static constexpr int kABufs0 = 3;
-    static constexpr int kBudget = 232448 - 2048;
-    static constexpr int kLoadBytes = kXBytes + kPBytes;
-    static constexpr int kStagesRaw = kSplitRing ? (kBudget - kABufs0 * kPairABytes) / kLoadBytes
-                                                 : kBudget / (kLoadBytes + kPairABytes);
-    static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
-    static constexpr int kABufs = kSplitRing ? kABufs0 : kStages;
-    static constexpr int kSmemBytes = kStages * kLoadBytes + kABufs * kPairABytes + 1024 + 1024;
-    static constexpr int kTmemCols = 2 * kMmaN;
-    static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "TMEM columns");
-    static_assert(kStages >= 2 && kABufs >= 2 && kSmemBytes <= 232448, "shared memory");
+// Blocks of 64 that one code unit covers, and its bytes.
+template <int BITS, bool DGRAD>
+struct PairUnit {
+    static constexpr int kBlocks = (!DGRAD && BITS == 4) ? 2 : 1;
+    static constexpr int kBytes = 2 * kPairRows * kPairBlock * BITS / 8 * kBlocks;
+    static constexpr int kSlots = kPairPBytes / kBytes;
+    static_assert(kSlots >= 3, "code ring");
 };
 
 struct PairArgs {
@@ -184,7 +194,7 @@ struct PairArgs {
     uint16_t* out;               // GATED: H [M, N]; DGRAD: dX [M, K]
     uint16_t* G;                 // GATED: kept outputs, or null
     uint16_t* U;
-    float* partials;             // split reduction: fp32 parts, or null
+    float* partials;             // split reduction: binary32 parts
     int M, N, K;
     int gshift;                  // log2 g; 31 for per-channel (one group per row)
     int groups;                  // groups per row
@@ -192,8 +202,58 @@ struct PairArgs {
     float zsym;                  // symmetric codes: 8 or 128 (the flipped code of 0), else 0
     int act;
     int products;                // DGRAD: 1 or 2
-    int blocks;                  // reduction blocks in all
-    int blocks_split;            // per split
+    int bt;                      // tokens of a CTA's tile (PAIR: half of the tile's)
+    int acc_cols;                // tensor-memory columns of one accumulator (power of two)
+    int blocks;                  // reduction blocks of a tile
+    int tiles_m;
+    int whole;                   // tiles [0, whole) are computed whole, dealt in turn
+    int tiles;                   // the others [whole, tiles) are split evenly ...
+    int sharers;                 // ... over this many CTAs (pairs), in code units; 0: none
+};
+
+// A CTA's (pair's) share of the work: whole tiles first, then its range of the split
+// tiles' units, as segments (tile, first unit, units).
+template <int UB>
+struct PairWalk {
+    int slots, slot, upt;        // CTAs (pairs), this one, units per tile
+    int tile, u0, units;
+    int64_t at, end;             // split range still to do
+    int part;                    // index of a split segment's part, -1 for a whole tile
+    __device__ __forceinline__ void init(const PairArgs& a, int slots_, int slot_) {
+        slots = slots_;
+        slot = slot_;
+        upt = (a.blocks + UB - 1) / UB;
+        tile = slot - slots;
+        at = end = 0;
+        if (a.sharers > 0 && slot < a.sharers) {
+            const int64_t total = (int64_t)(a.tiles - a.whole) * upt;
+            at = total * slot / a.sharers;
+            end = total * (slot + 1) / a.sharers;
+        }
+        part = -1;
+    }
+    __device__ __forceinline__ bool next(const PairArgs& a) {
+        if (part < 0) {
+            tile += slots;
+            if (tile < a.whole) {
+                u0 = 0;
+                units = upt;
+                return true;
+            }
+        }
+        if (at >= end) return false;
+        ++part;                              // 0, then 1
+        tile = a.whole + (int)(at / upt);
+        u0 = (int)(at % upt);
+        units = (int)(end - at < upt - u0 ? end - at : upt - u0);
+        at += units;
+        return true;
+    }
+    __device__ __forceinline__ int first_block() const { return u0 * UB; }
+    __device__ __forceinline__ int count(const PairArgs& a) const {
+        const int last = (u0 + units) * UB;
+        return (last < a.blocks ? last : a.blocks) - u0 * UB;
+    }
 };
 
 // Zero point as the dequantization wants it: the bf16 pair of 128 + z (4-bit codes), or
@@ -205,18 +265,22 @@ __device__ __forceinline__ uint32_t pair_zero(uint32_t z_bits, bool sym, float z
     return __float_as_uint(8388608.0f + z);
 }
 
-// 32 codes (4-bit: one 16-byte chunk; 8-bit: two) of one scale group -> 16 bf16 pairs.
+// Eight codes -> four bf16 pairs in natural order.  4 bits (w0): PRMT brings code 2j of
+// the word and code 2j + 1 of the word shifted by 4 into the low bytes of the halves, one
+// LOP3 masks the nibbles and sets the exponent of 128 (symmetric codes: bit 3 flipped in
+// the same LOP3).  8 bits (w0, w1): as dequant4_bytes in gemm_tcgen05.cuh.
 template <int BITS>
 __device__ __forceinline__ void pair_dequant8(uint32_t w0, uint32_t w1, uint32_t flip, uint32_t zz,
                                               uint32_t s_bits, uint32_t out[4]) {
     if constexpr (BITS == 4) {
-        const uint32_t ss = dup16(s_bits);
-        const uint32_t lo = (w0 ^ flip) & 0x0F0F0F0Fu;
-        const uint32_t hi = ((w0 ^ flip) >> 4) & 0x0F0F0F0Fu;
+        const uint32_t ss = dup16(s_bits), magic = 0x43004300u | (flip & 0x00080008u), hi = w0 >> 4;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t sel = (uint32_t)j | 0x80u | ((uint32_t)(4 + j) << 8) | 0xC000u;
-            out[j] = bf16x2_mul(bf16x2_sub(isolate_magic<false>(__byte_perm(lo, hi, sel), 0x000F000Fu), zz), ss);
+            // bytes: [w.j, any, (w >> 4).j, any]
+            const uint32_t sel = (uint32_t)j | ((uint32_t)j << 4) | ((uint32_t)(4 + j) << 8) | ((uint32_t)(4 + j) << 12);
+            uint32_t q;
+            asm("lop3.b32 %0, %1, 0x000F000F, %2, 0x6A;" : "=r"(q) : "r"(__byte_perm(w0, hi, sel)), "r"(magic));
+            out[j] = bf16x2_mul(bf16x2_sub(q, zz), ss);
         }
     } else {
         const float s = bf16_bits_to_f32(s_bits), zoff = __uint_as_float(zz);
@@ -239,385 +303,560 @@ __device__ __forceinline__ void sts128_addr(uint32_t addr, const uint32_t v[4]) 
                  : "memory");
 }
 
-// Feature (GATED) or input channel (DGRAD) of row r of accumulator j of a CTA.
-template <bool DGRAD>
-__device__ __forceinline__ int pair_row(int r0, int rank, int j, int r) {
-    return DGRAD ? r0 + rank * 2 * kPairRows + j * kPairRows + r : r0 + rank * kPairRows + r;
+__device__ __forceinline__ uint4 lds128_addr(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
 }
 
-// One finished 32-token strip of a row: g (and u) hold the accumulators' values.
-template <bool DGRAD>
-__device__ __forceinline__ void pair_store(const PairArgs& a, int row0, int row1, int m, float v0, float v1) {
-    if constexpr (DGRAD) {
-        const int64_t at = (int64_t)m * a.K;
-        if (row0 < a.K) a.out[at + row0] = (uint16_t)f32_to_bf16_bits_rn(v0);
-        if (row1 < a.K) a.out[at + row1] = (uint16_t)f32_to_bf16_bits_rn(v1);
-    } else {
-        if (row0 >= a.N) return;
-        const int64_t at = (int64_t)m * a.N + row0;
-        a.out[at] = (uint16_t)f32_to_bf16_bits_rn(act_value(a.act, v0) * v1);
-        if (a.G != nullptr) {
-            a.G[at] = (uint16_t)f32_to_bf16_bits_rn(v0);
-            a.U[at] = (uint16_t)f32_to_bf16_bits_rn(v1);
+// ------------------------------------------------------------------ epilogue
+// A strip is 32 rows (a warp's quarter of tensor memory) x 16 tokens.  tcgen05.ld
+// 16x256b gives it as MMA fragments (lane t: rows t/4 and t/4 + 8, tokens 2(t%4), + 1), so
+// that stmatrix can transpose it: the strip goes through 1 KB of shared memory as 16
+// token rows of 32 contiguous outputs and leaves in 16-byte stores.  Storing a
+// lane's row directly took 32 two-byte stores per lane and output instead of 2.
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t r[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(r0),
+                 "r"(r1), "r"(r2), "r"(r3)
+                 : "memory");
+}
+
+// Rounds a strip to bf16 and writes it to out[m0 .. m0+15][c0 .. c0+31] (rows of `ld`
+// elements, `cols` of them valid, M rows).  v[8h + i]: register i of row half h.
+__device__ __forceinline__ void strip_store(const float v[16], uint32_t stage, uint16_t* __restrict__ out, int m0, int M,
+                                            int c0, int cols, int lane) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        // matrices: (rows 0-7, tokens 0-7), (rows 8-15, tokens 0-7), then tokens 8-15
+        const int token = (lane & 7) + 8 * (lane >> 4);
+        const int chunk = 2 * h + ((lane >> 3) & 1);
+        stmatrix_x4_trans(stage + (uint32_t)(token * 64 + ((chunk ^ ((token >> 1) & 3)) * 16)),
+                          pack_bf16(v[8 * h], v[8 * h + 1]), pack_bf16(v[8 * h + 2], v[8 * h + 3]),
+                          pack_bf16(v[8 * h + 4], v[8 * h + 5]), pack_bf16(v[8 * h + 6], v[8 * h + 7]));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int token = (lane >> 2) + 8 * i, chunk = lane & 3;
+        const uint4 d = lds128_addr(stage + (uint32_t)(token * 64 + ((chunk ^ ((token >> 1) & 3)) * 16)));
+        const int m = m0 + token, c = c0 + 8 * chunk;
+        if (m < M && c < cols) {
+            uint16_t* o = out + (int64_t)m * cols + c;
+            if ((cols & 7) == 0) {
+                *reinterpret_cast<uint4*>(o) = d;
+            } else {
+                const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < cols) o[e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+            }
         }
+    }
+    __syncwarp();                                   // the staging bytes are free again
+}
+
+// Both accumulators' strips of rows row0 + 32·quarter .. + 31.
+template <bool DGRAD>
+__device__ __forceinline__ void pair_emit(const PairArgs& a, float v0[16], float v1[16], uint32_t stage, int r0, int rank,
+                                          int quarter, int m, int lane) {
+    if constexpr (DGRAD) {
+        const int c = r0 + rank * 2 * kPairRows + 32 * quarter;
+        strip_store(v0, stage, a.out, m, a.M, c, a.K, lane);
+        strip_store(v1, stage, a.out, m, a.M, c + kPairRows, a.K, lane);
+    } else {
+        const int c = r0 + rank * kPairRows + 32 * quarter;
+        if (a.G != nullptr) {
+            strip_store(v0, stage, a.G, m, a.M, c, a.N, lane);
+            strip_store(v1, stage, a.U, m, a.M, c, a.N, lane);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v0[i] = act_value(a.act, v0[i]) * v1[i];
+        strip_store(v0, stage, a.out, m, a.M, c, a.N, lane);
     }
 }
 
-template <int BT, bool PAIR, int BITS, bool DGRAD>
+// First row of a tile (features or input channels) and its first token.
+template <bool DGRAD>
+__device__ __forceinline__ int pair_row0(const PairArgs& a, int tile, int ctas) {
+    return tile / a.tiles_m * (DGRAD ? 2 : 1) * ctas * kPairRows;
+}
+
+// Floats of one CTA's part: [strip of 16 tokens][quarter][accumulator][4][lane] float4.
+__host__ __device__ inline int64_t pair_part_floats(int tokens) {
+    return (int64_t)((tokens + 15) / 16) * 4 * 2 * 16 * 32;
+}
+
+template <bool PAIR, int BITS, bool DGRAD>
 __global__ void __launch_bounds__(kPairThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmX0, const __grid_constant__ CUtensorMap tmX1,
                      const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmP1,
                      const PairArgs a) {
-    using Cfg = PairConfig<BT, PAIR, BITS>;
-    constexpr int S = Cfg::kStages, NA = Cfg::kABufs;
-    constexpr bool kSplit = Cfg::kSplitRing;
+    using Unit = PairUnit<BITS, DGRAD>;
+    constexpr int UB = Unit::kBlocks, SP = Unit::kSlots, NA = kPairABufs;
     constexpr int kCtas = PAIR ? 2 : 1;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t* as = smem;                              // NA x kPairABytes
-    uint8_t* xs = as + NA * kPairABytes;             // S x kXBytes
-    uint8_t* ps = xs + S * Cfg::kXBytes;             // S x kPBytes
-    uint64_t* full = reinterpret_cast<uint64_t*>(ps + S * Cfg::kPBytes);
-    uint64_t* empty = full + S;
-    uint64_t* afull = empty + S;
-    uint64_t* aempty = afull + NA;
-    uint64_t* accf = aempty + NA;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(accf + 1);
+    const uint32_t as = smem_u32(smem);              // NA x kPairABytes
+    const uint32_t xs = as + NA * kPairABytes;       // token ring: SX x bt x 128 bytes
+    const uint32_t ps = xs + kPairXBytes;            // SP code units
+    const uint32_t st = ps + kPairPBytes;            // epilogue staging
+    const uint32_t bars = st + kPairStageBytes;
+    const int x_bytes = a.bt * kPairBlock * 2;
+    const int SX = min(kPairXBytes / x_bytes, kPairMaxX);
+    const uint32_t xfull = bars, xempty = xfull + 8 * kPairMaxX;
+    const uint32_t pfull = xempty + 8 * kPairMaxX, pempty = pfull + 8 * SP;
+    const uint32_t afull = pempty + 8 * SP, aempty = afull + 8 * NA;
+    const uint32_t accf = aempty + 8 * NA;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + (accf + 8 - as));
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
-    const int tile = (int)blockIdx.x / kCtas;
-    const int tokens = kCtas * BT;
-    const int tiles_m = (a.M + tokens - 1) / tokens;
-    const int m0 = (tile % tiles_m) * tokens;
-    const int r0 = (tile / tiles_m) * (DGRAD ? 2 : 1) * kCtas * kPairRows;
-    const int b0 = (int)blockIdx.y * a.blocks_split;
-    const int nb = min(a.blocks - b0, a.blocks_split);
+    const int slots = (int)gridDim.x / kCtas, slot = (int)blockIdx.x / kCtas;
     const int per_product = a.blocks / a.products;
+    const int mma_n = kCtas * a.bt;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&full[s]), 1);
-            mbar_init(smem_u32(&empty[s]), kSplit ? 1 + kPairDequantWarps : 1);
+        for (int s = 0; s < SX; ++s) {
+            mbar_init(xfull + 8 * s, 1);
+            mbar_init(xempty + 8 * s, 1);
+        }
+        for (int s = 0; s < SP; ++s) {
+            mbar_init(pfull + 8 * s, 1);
+            mbar_init(pempty + 8 * s, kPairDequantWarps);
         }
         for (int s = 0; s < NA; ++s) {
-            mbar_init(smem_u32(&afull[s]), kCtas * kPairDequantWarps);
-            mbar_init(smem_u32(&aempty[s]), 1);
+            mbar_init(afull + 8 * s, kCtas * kPairDequantWarps);
+            mbar_init(aempty + 8 * s, 1);
         }
-        mbar_init(smem_u32(accf), 1);
+        mbar_init(accf, 1);
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
         prefetch_tensormap(&tmX0);
-        prefetch_tensormap(&tmP0);
-        if (!DGRAD || a.products > 1) prefetch_tensormap(&tmP1);
         if (DGRAD && a.products > 1) prefetch_tensormap(&tmX1);
     }
-    if (warp == 1) tmem_alloc_g<PAIR>(smem_u32(tmem_holder), Cfg::kTmemCols);
+    if (warp == kPairCodeWarp && lane == 0) {
+        prefetch_tensormap(&tmP0);
+        if (!DGRAD || a.products > 1) prefetch_tensormap(&tmP1);
+    }
+    if (warp == 1) tmem_alloc_g<PAIR>(smem_u32(tmem_holder), 2 * a.acc_cols);
     tc_fence_before();
     __syncwarp();
+    __syncthreads();
     if constexpr (PAIR) cluster_sync_all();      // the pair's barriers are set up before either arrives
-    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem_d = *tmem_holder;
+    PairWalk<UB> walk;
+    walk.init(a, slots, slot);
 
     if (warp == 0) {
-        // ------------------------------------------------------------ loads
+        // ------------------------------------------------------------ token loads
         if (lane == 0) {
-            int issued = 0;
-            for (int i = 0; i < nb; ++i) {
-                const int s = i % S;
-                if (!mbar_wait(smem_u32(&empty[s]), ((uint32_t)(i / S) & 1u) ^ 1u)) break;
-                const uint32_t bar = smem_u32(&full[s]);
-                const uint32_t x = smem_u32(xs + s * Cfg::kXBytes), p = smem_u32(ps + s * Cfg::kPBytes);
-                mbar_arrive_expect_tx(bar, Cfg::kXBytes + Cfg::kPBytes);
-                if constexpr (DGRAD) {
-                    const int b = b0 + i, prod = b / per_product, n = (b - prod * per_product) * kPairBlock;
-                    const CUtensorMap* tx = prod ? &tmX1 : &tmX0;
-                    const CUtensorMap* tp = prod ? &tmP1 : &tmP0;
-                    tma_load_2d(x, tx, n, m0 + rank * BT, bar);
-                    const int c0 = (r0 + rank * 2 * kPairRows) * BITS / 8;   // code bytes; boxes of 128
-#pragma unroll
-                    for (int h = 0; h < BITS / 4; ++h)
-                        tma_load_2d(p + h * kPairBlock * 128, tp, c0 + 128 * h, n, bar);
-                } else {
-                    const int k = (b0 + i) * kPairBlock;
-                    tma_load_2d(x, &tmX0, k, m0 + rank * BT, bar);
-                    tma_load_2d(p, &tmP0, k * BITS / 8, r0 + rank * kPairRows, bar);
-                    tma_load_2d(p + Cfg::kPBytes / 2, &tmP1, k * BITS / 8, r0 + rank * kPairRows, bar);
+            int s = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            while (ok && walk.next(a)) {
+                const int b0 = walk.first_block(), nb = walk.count(a);
+                const int m0 = walk.tile % a.tiles_m * mma_n + rank * a.bt;
+                for (int i = 0; i < nb; ++i) {
+                    ok = mbar_wait(xempty + 8 * s, ph ^ 1u);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(xfull + 8 * s, x_bytes);
+                    int b = b0 + i;
+                    const CUtensorMap* tx = &tmX0;
+                    if (DGRAD && b >= per_product) {
+                        b -= per_product;
+                        tx = &tmX1;
+                    }
+                    tma_load_2d(xs + s * x_bytes, tx, b * kPairBlock, m0, xfull + 8 * s);
+                    ++issued;
+                    if (++s == SX) { s = 0; ph ^= 1u; }
                 }
-                ++issued;
             }
             // Do not leave while copies into this CTA's shared memory are in flight.
-            for (int i = (issued > S ? issued - S : 0); i < issued; ++i)
-                if (!mbar_wait(smem_u32(&full[i % S]), (uint32_t)(i / S) & 1u)) break;
+            for (int i = (issued > SX ? issued - SX : 0); i < issued; ++i)
+                if (!mbar_wait(xfull + 8 * (i % SX), (uint32_t)(i / SX) & 1u)) break;
+        }
+        __syncwarp();
+    } else if (warp == kPairCodeWarp) {
+        // ------------------------------------------------------------ code loads
+        if (lane == 0) {
+            int s = 0, issued = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            while (ok && walk.next(a)) {
+                const int r0 = pair_row0<DGRAD>(a, walk.tile, kCtas);
+                for (int u = 0; u < walk.units; ++u) {
+                    ok = mbar_wait(pempty + 8 * s, ph ^ 1u);
+                    if (!ok) break;
+                    const uint32_t bar = pfull + 8 * s, p = ps + s * Unit::kBytes;
+                    mbar_arrive_expect_tx(bar, Unit::kBytes);
+                    if constexpr (DGRAD) {
+                        int b = walk.u0 + u;
+                        const CUtensorMap* tp = &tmP0;
+                        if (b >= per_product) {
+                            b -= per_product;
+                            tp = &tmP1;
+                        }
+                        const int c0 = (r0 + rank * 2 * kPairRows) * BITS / 8;   // code bytes; boxes of 128
+#pragma unroll
+                        for (int h = 0; h < BITS / 4; ++h)
+                            tma_load_2d(p + h * kPairBlock * 128, tp, c0 + 128 * h, b * kPairBlock, bar);
+                    } else {
+                        const int k = (walk.u0 + u) * UB * kPairBlock, n = r0 + rank * kPairRows;
+                        tma_load_2d(p, &tmP0, k * BITS / 8, n, bar);
+                        tma_load_2d(p + Unit::kBytes / 2, &tmP1, k * BITS / 8, n, bar);
+                    }
+                    ++issued;
+                    if (++s == SP) { s = 0; ph ^= 1u; }
+                }
+            }
+            for (int i = (issued > SP ? issued - SP : 0); i < issued; ++i)
+                if (!mbar_wait(pfull + 8 * (i % SP), (uint32_t)(i / SP) & 1u)) break;
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issue (even CTA)
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = idesc_bf16_f32(kCtas * kPairRows, Cfg::kMmaN) |
-                                       (DGRAD ? kIdescAMnMajor : 0u);
-            for (int i = 0; i < nb; ++i) {
-                const int s = i % S, ab = i % NA;
-                // (the dequantizers arrive after the stage's loads landed, X among them)
-                if (!mbar_wait_cluster(smem_u32(&afull[ab]), (uint32_t)(i / NA) & 1u)) break;
-                tc_fence_after();
-                const uint32_t at = smem_u32(as + ab * kPairABytes);
-                const uint32_t xt = smem_u32(xs + s * Cfg::kXBytes);
+            const uint32_t idesc = idesc_bf16_f32(kCtas * kPairRows, mma_n) | (DGRAD ? kIdescAMnMajor : 0u);
+            int s = 0, ab = 0;
+            uint32_t pa = 0;
+            bool ok = true;
+            while (ok && walk.next(a)) {
+                const int nb = walk.count(a);
+                for (int i = 0; i < nb; ++i) {
+                    // (a dequantizing warp of each CTA arrives after the tokens landed there too)
+                    ok = mbar_wait_cluster(afull + 8 * ab, pa);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t at = as + ab * kPairABytes, xt = xs + s * x_bytes;
 #pragma unroll
-                for (int kk = 0; kk < kPairBlock / 16; ++kk) {
-                    const uint64_t bd = sw128_kmajor_desc(xt + kk * 32);
+                    for (int kk = 0; kk < kPairBlock / 16; ++kk) {
+                        const uint64_t bd = sw128_kmajor_desc(xt + kk * 32);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t aj = at + j * (kPairABytes / 2);
-                        const uint64_t ad = DGRAD ? sw128_mnmajor_desc(aj + kk * 2048, 8192)
-                                                  : sw128_kmajor_desc(aj + kk * 32);
-                        tc_mma_bf16_g<PAIR>(tmem_d + (uint32_t)(j * Cfg::kMmaN), ad, bd, idesc,
-                                            (i | kk) != 0 ? 1u : 0u);
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t aj = at + j * (kPairABytes / 2);
+                            const uint64_t ad = DGRAD ? sw128_mnmajor_desc(aj + kk * 2048, 8192)
+                                                      : sw128_kmajor_desc(aj + kk * 32);
+                            tc_mma_bf16_g<PAIR>(tmem_d + (uint32_t)(j * a.acc_cols), ad, bd, idesc,
+                                                (i | kk) != 0 ? 1u : 0u);
+                        }
                     }
+                    tc_commit_g<PAIR>(xempty + 8 * s);
+                    tc_commit_g<PAIR>(aempty + 8 * ab);
+                    if (++s == SX) s = 0;
+                    if (++ab == NA) { ab = 0; pa ^= 1u; }
                 }
-                tc_commit_g<PAIR>(smem_u32(&empty[s]));
-                if (kSplit) tc_commit_g<PAIR>(smem_u32(&aempty[ab]));
+                tc_commit_g<PAIR>(accf);         // also on the error path: no MMA outlives the CTA
             }
-            tc_commit_g<PAIR>(smem_u32(accf));   // also on the error path: no MMA outlives the CTA
         }
         __syncwarp();
     } else {
-        // ------------------------------------------------------------ dequantize
+        // ------------------------------------------------------------ dequantize, epilogue
         const int w = warp - 2;
         const bool sym = a.flip != 0u;
+        const uint32_t afull_r = PAIR ? mapa_u32(afull, 0) : afull;
+        int xslot = 0, ab = 0, pslot = 0, seg = 0;
+        uint32_t xph = 0, aph = 0, pph = 0;
         bool ok = true;
-        auto release = [&](int s, int ab) {
+        // The A tiles of a block are written: visible to the tensor core, then counted.
+        auto release = [&]() {
             fence_proxy_async_smem();
             __syncwarp();
+            // one warp per CTA also vouches for the block's tokens
+            if (w == 0) ok = mbar_wait(xfull + 8 * xslot, xph) && ok;
             if (lane == 0) {
-                if constexpr (PAIR) mbar_arrive_cluster(mapa_u32(smem_u32(&afull[ab]), 0));
-                else mbar_arrive(smem_u32(&afull[ab]));
-                if (kSplit) mbar_arrive(smem_u32(&empty[s]));
+                if constexpr (PAIR) mbar_arrive_cluster(afull_r + 8 * ab);
+                else mbar_arrive(afull_r + 8 * ab);
             }
+            if (++xslot == SX) { xslot = 0; xph ^= 1u; }
+            if (++ab == NA) { ab = 0; aph ^= 1u; }
         };
-        if constexpr (!DGRAD) {
-            // thread = row r of both tiles, 32-wide half h of the block
-            const int r = (warp & 3) * 32 + lane, h = w >> 2;
-            const int n = r0 + rank * kPairRows + r;
-            const bool row_ok = n < a.N;
-            const bool vec = (a.groups & 7) == 0;             // rows of scales are 16-byte aligned
-            int have = -1;                                    // the group whose pair is in sg, zg
-            uint32_t sg[2] = {0u, 0u}, zg[2] = {0u, 0u};
-            uint4 sv[2], zv[2];
-            for (int i = 0; i < nb; ++i) {
-                const int s = i % S, ab = i % NA;
-                const int k = (b0 + i) * kPairBlock + 32 * h;
-                const int grp = min(k >> a.gshift, a.groups - 1);
-                if (grp != have) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t sb = 0u, zb = 0u;
-                        if (vec) {
-                            if (have < 0 || (grp >> 3) != (have >> 3)) {
-                                const int64_t at = (int64_t)n * a.groups + (grp & ~7);
-                                sv[j] = row_ok ? ldg_cached(a.scales[j] + at) : make_uint4(0, 0, 0, 0);
-                                zv[j] = row_ok && !sym ? ldg_cached(a.zeros[j] + at) : make_uint4(0, 0, 0, 0);
-                            }
-                            const int q = grp & 7;
-                            const uint32_t sw = q < 4 ? (q < 2 ? sv[j].x : sv[j].y) : (q < 6 ? sv[j].z : sv[j].w);
-                            const uint32_t zw = q < 4 ? (q < 2 ? zv[j].x : zv[j].y) : (q < 6 ? zv[j].z : zv[j].w);
-                            sb = (sw >> (16 * (q & 1))) & 0xFFFFu;
-                            zb = (zw >> (16 * (q & 1))) & 0xFFFFu;
-                        } else if (row_ok) {
-                            const int64_t at = (int64_t)n * a.groups + grp;
-                            sb = ldg_u16(a.scales[j] + at);
-                            if (!sym) zb = ldg_u16(a.zeros[j] + at);
+        // The next unit's codes are read from the slot behind; a slot is given back only once
+        // the codes were used.  (Given back right behind the loads, a slot was seen refilled
+        // before a load of it had been performed: the load's value is needed first.)
+        int pdone = 0;
+        auto unit_next = [&]() {
+            if (++pslot == SP) { pslot = 0; pph ^= 1u; }
+        };
+        auto unit_done = [&]() {                 // behind release(): all lanes used their codes
+            if (lane == 0) mbar_arrive(pempty + 8 * pdone);
+            if (++pdone == SP) pdone = 0;
+        };
+        while (ok && walk.next(a)) {
+            const int r0 = pair_row0<DGRAD>(a, walk.tile, kCtas);
+            const int b0 = walk.first_block(), nb = walk.count(a);
+            if constexpr (!DGRAD) {
+                // thread = row r of matrix j, 32-wide half h of the block
+                const int j = w >> 3, r = (w & 3) * 32 + lane, h = (w >> 2) & 1;
+                const int n = r0 + rank * kPairRows + r;
+                const bool row_ok = n < a.N;
+                const bool vec = (a.groups & 7) == 0;         // rows of scales are 16-byte aligned
+                const uint16_t* sp = (j ? a.scales[1] : a.scales[0]) + (int64_t)(row_ok ? n : 0) * a.groups;
+                const uint16_t* zp = (sym ? sp : (j ? a.zeros[1] : a.zeros[0]) + (int64_t)(row_ok ? n : 0) * a.groups);
+                // the eight groups around the current one, and the next eight
+                uint4 sv = make_uint4(0, 0, 0, 0), zv = sv, sn = sv, zn = sv;
+                int have = -1;
+                uint32_t sg = 0u, zg = 0u, sraw = 0u, zraw = 0u;
+                auto slab = [&](int grp, uint4& s8, uint4& z8) {
+                    if (row_ok && grp < a.groups) {
+                        s8 = ldg_cached(sp + grp);
+                        if (!sym) z8 = ldg_cached(zp + grp);
+                    }
+                };
+                auto single = [&](int grp) {
+                    if (row_ok && grp < a.groups) {
+                        sraw = ldg_u16(sp + grp);
+                        if (!sym) zraw = ldg_u16(zp + grp);
+                    }
+                };
+                {
+                    const int g0 = min((b0 * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
+                    if (vec) slab(g0 & ~7, sn, zn);
+                    else single(g0);
+                }
+                auto scales_of = [&](int i) {
+                    const int grp = min(((b0 + i) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
+                    if (grp == have) return;
+                    uint32_t sb, zb;
+                    if (vec) {
+                        if (have < 0 || (grp >> 3) != (have >> 3)) {
+                            sv = sn;
+                            zv = zn;
+                            slab((grp & ~7) + 8, sn, zn);
                         }
-                        sg[j] = sb;
-                        zg[j] = pair_zero<BITS>(zb, sym, a.zsym);
-                    }
-                    have = grp;
-                }
-                if (!mbar_wait(smem_u32(&full[s]), (uint32_t)(i / S) & 1u)) {
-                    ok = false;
-                    break;
-                }
-                if (kSplit && !mbar_wait(smem_u32(&aempty[ab]), ((uint32_t)(i / NA) & 1u) ^ 1u)) {
-                    ok = false;
-                    break;
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint8_t* prow = ps + s * Cfg::kPBytes + j * (Cfg::kPBytes / 2) + r * (kPairBlock * BITS / 8);
-                    uint4 v, v8 = make_uint4(0, 0, 0, 0);
-                    if constexpr (BITS == 4) {
-                        v = lds128(prow + 16 * (h ^ ((r >> 2) & 1)));           // 32-byte swizzle
+                        const int q = grp & 7;
+                        const uint32_t sw = q < 4 ? (q < 2 ? sv.x : sv.y) : (q < 6 ? sv.z : sv.w);
+                        const uint32_t zw = q < 4 ? (q < 2 ? zv.x : zv.y) : (q < 6 ? zv.z : zv.w);
+                        sb = (sw >> (16 * (q & 1))) & 0xFFFFu;
+                        zb = (zw >> (16 * (q & 1))) & 0xFFFFu;
                     } else {
-                        v = lds128(prow + 16 * ((2 * h) ^ ((r >> 1) & 3)));     // 64-byte swizzle
-                        v8 = lds128(prow + 16 * ((2 * h + 1) ^ ((r >> 1) & 3)));
+                        sb = sraw;
+                        zb = zraw;
+                        single(((b0 + i + 1) * kPairBlock + 32 * h) >> a.gshift == grp
+                                   ? grp + 1
+                                   : min(((b0 + i + 1) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1));
                     }
-                    const uint32_t wv[8] = {v.x, v.y, v.z, v.w, v8.x, v8.y, v8.z, v8.w};
-                    const uint32_t arow = smem_u32(as + ab * kPairABytes + j * (kPairABytes / 2)) + r * 128;
+                    sg = sb;
+                    zg = pair_zero<BITS>(zb, sym, a.zsym);
+                    have = grp;
+                };
+                constexpr int kRowBytes = kPairBlock * UB * BITS / 8;      // 64
+                uint4 c0v, c1v = make_uint4(0, 0, 0, 0);
+                auto codes_of = [&](int i) {
+                    if (i % UB == 0) ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
+                    const uint32_t row = ps + pslot * Unit::kBytes + j * (Unit::kBytes / 2) + r * kRowBytes;
+                    if constexpr (BITS == 4) {
+                        c0v = lds128_addr(row + (uint32_t)(((2 * (i % UB) + h) ^ ((r >> 1) & 3)) * 16));
+                    } else {
+                        c0v = lds128_addr(row + (uint32_t)(((2 * h) ^ ((r >> 1) & 3)) * 16));
+                        c1v = lds128_addr(row + (uint32_t)(((2 * h + 1) ^ ((r >> 1) & 3)) * 16));
+                    }
+                    if (i % UB == UB - 1 || i == nb - 1) unit_next();
+                };
+                codes_of(0);
+                for (int i = 0; i < nb && ok; ++i) {
+                    const uint32_t wv[8] = {c0v.x, c0v.y, c0v.z, c0v.w, c1v.x, c1v.y, c1v.z, c1v.w};
+                    scales_of(i);
+                    if (i + 1 < nb) codes_of(i + 1);
+                    ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
+                    if (!ok) break;
+                    const uint32_t arow = as + ab * kPairABytes + j * (kPairABytes / 2) + r * 128;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         uint32_t d[4];
-                        if constexpr (BITS == 4) pair_dequant8<4>(wv[c], 0u, a.flip, zg[j], sg[j], d);
-                        else pair_dequant8<8>(wv[2 * c], wv[2 * c + 1], a.flip, zg[j], sg[j], d);
+                        if constexpr (BITS == 4) pair_dequant8<4>(wv[c], 0u, a.flip, zg, sg, d);
+                        else pair_dequant8<8>(wv[2 * c], wv[2 * c + 1], a.flip, zg, sg, d);
                         sts128_addr(arow + (uint32_t)(((4 * h + c) ^ (r & 7)) * 16), d);
                     }
+                    release();
+                    if (i % UB == UB - 1 || i == nb - 1) unit_done();
                 }
-                release(s, ab);
-            }
-        } else {
-            // thread = weight row r of the block, 64-channel block q: the four threads of a row
-            // are neighbours, so that a warp's scale loads touch eight rows.  Each starts
-            // at another chunk (2q), which keeps its shared-memory stores off the
-            // banks of the other three.
-            const int r = w * 8 + (lane >> 2), q = lane & 3;
-            const int c0 = r0 + rank * 2 * kPairRows + 64 * q;       // first input channel
-            const bool chan_ok = c0 < a.K;
-            const int g0 = min(c0 >> a.gshift, a.groups - 1), g1 = min((c0 + 32) >> a.gshift, a.groups - 1);
-            // scales and zeros of the next blocks, two ahead (raw bf16 bits)
-            uint32_t sn[2][2], zn[2][2];
-            auto fetch = [&](int i, uint32_t* sb, uint32_t* zb) {
-                const int b = b0 + i, prod = b / per_product, n = (b - prod * per_product) * kPairBlock + r;
-                sb[0] = sb[1] = zb[0] = zb[1] = 0u;
-                if (i < nb && n < a.N && chan_ok) {
-                    const uint16_t* sp = prod ? a.scales[1] : a.scales[0];
-                    const uint16_t* zp = prod ? a.zeros[1] : a.zeros[0];
-                    const int64_t at = (int64_t)n * a.groups;
-                    sb[0] = ldg_u16(sp + at + g0);
-                    if (!sym) zb[0] = ldg_u16(zp + at + g0);
-                    sb[1] = sb[0];
-                    zb[1] = zb[0];
-                    if (g1 != g0) {
-                        sb[1] = ldg_u16(sp + at + g1);
-                        if (!sym) zb[1] = ldg_u16(zp + at + g1);
+            } else {
+                // thread = weight row r of the block, 32-channel piece q: the eight threads of a
+                // row are neighbours, so that a warp's scale loads touch four rows.  Those that
+                // store into the same banks (64 channels apart) take their four chunks in
+                // rotated order.
+                const int r = w * 4 + (lane >> 3), q = lane & 7, rot = q >> 1;
+                const int c0 = r0 + rank * 2 * kPairRows + 32 * q;       // first input channel
+                const bool chan_ok = c0 < a.K;
+                const int grp = min(c0 >> a.gshift, a.groups - 1);
+                auto fetch = [&](int i, uint32_t& sb, uint32_t& zb) {
+                    sb = zb = 0u;
+                    int b = b0 + i;
+                    const bool second = b >= per_product;
+                    if (second) b -= per_product;
+                    const int n = b * kPairBlock + r;
+                    if (i < nb && n < a.N && chan_ok) {
+                        const int64_t at = (int64_t)n * a.groups + grp;
+                        sb = ldg_u16((second ? a.scales[1] : a.scales[0]) + at);
+                        if (!sym) zb = ldg_u16((second ? a.zeros[1] : a.zeros[0]) + at);
                     }
-                }
-            };
-            fetch(0, sn[0], zn[0]);
-            fetch(1, sn[1], zn[1]);
-            for (int i = 0; i < nb; ++i) {
-                const int s = i % S, ab = i % NA;
-                const uint32_t s0 = sn[0][0], s1 = sn[0][1];
-                const uint32_t z0 = pair_zero<BITS>(zn[0][0], sym, a.zsym), z1 = pair_zero<BITS>(zn[0][1], sym, a.zsym);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    sn[0][t] = sn[1][t];
-                    zn[0][t] = zn[1][t];
-                }
-                fetch(i + 2, sn[1], zn[1]);
-                if (!mbar_wait(smem_u32(&full[s]), (uint32_t)(i / S) & 1u)) {
-                    ok = false;
-                    break;
-                }
-                if (kSplit && !mbar_wait(smem_u32(&aempty[ab]), ((uint32_t)(i / NA) & 1u) ^ 1u)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t line = smem_u32(as + ab * kPairABytes) + (uint32_t)(q * 8192 + r * 128);
-                const uint8_t* pst = ps + s * Cfg::kPBytes;
-                if constexpr (BITS == 4) {
-                    // 32 code bytes: logical chunks 2q, 2q + 1 of the row's eight (128-byte swizzle)
-                    const uint4 va = lds128(pst + r * 128 + (((2 * q) ^ (r & 7)) * 16));
-                    const uint4 vb = lds128(pst + r * 128 + (((2 * q + 1) ^ (r & 7)) * 16));
-                    uint32_t u[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w}, v[8];
-                    // u rotated by 2q words: step c handles chunk (c + 2q) mod 8
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) v[c] = (q & 2) ? u[(c + 4) & 7] : u[c];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) u[c] = (q & 1) ? v[(c + 2) & 7] : v[c];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const int ch = (c + 2 * q) & 7;
-                        uint32_t d[4];
-                        pair_dequant8<4>(u[c], 0u, a.flip, ch < 4 ? z0 : z1, ch < 4 ? s0 : s1, d);
-                        sts128_addr(line + (uint32_t)((ch ^ (r & 7)) * 16), d);
+                };
+                // pairs of the next three blocks
+                uint32_t s0, z0, s1, z1, s2, z2;
+                fetch(0, s0, z0);
+                fetch(1, s1, z1);
+                fetch(2, s2, z2);
+                uint4 c0v, c1v = make_uint4(0, 0, 0, 0);
+                auto codes_of = [&]() {
+                    ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
+                    const uint32_t row = ps + pslot * Unit::kBytes + r * 128;
+                    if constexpr (BITS == 4) {
+                        c0v = lds128_addr(row + (uint32_t)((q ^ (r & 7)) * 16));
+                    } else {
+                        // 32 bytes: chunks 2(q & 3), + 1 of box q / 4; the boxes read them in opposite order
+                        const uint32_t box = row + (uint32_t)(q >> 2) * (kPairBlock * 128);
+                        const int f = q >> 2;
+                        const uint4 e0 = lds128_addr(box + (uint32_t)(((2 * (q & 3) + f) ^ (r & 7)) * 16));
+                        const uint4 e1 = lds128_addr(box + (uint32_t)(((2 * (q & 3) + 1 - f) ^ (r & 7)) * 16));
+                        c0v = f ? e1 : e0;
+                        c1v = f ? e0 : e1;
                     }
-                } else {
-                    // 64 code bytes: chunks 4(q & 1) .. + 3 of the row in box q / 2
-                    const uint8_t* row = pst + (q >> 1) * (kPairBlock * 128) + r * 128;
+                    unit_next();
+                };
+                codes_of();
+                for (int i = 0; i < nb && ok; ++i) {
+                    uint32_t u[8] = {c0v.x, c0v.y, c0v.z, c0v.w, c1v.x, c1v.y, c1v.z, c1v.w};
+                    const uint32_t sg = s0, zg = pair_zero<BITS>(z0, sym, a.zsym);
+                    s0 = s1; z0 = z1;
+                    s1 = s2; z1 = z2;
+                    fetch(i + 3, s2, z2);
+                    if (i + 1 < nb) codes_of();
+                    // chunk c of the rotated order is chunk (c + rot) mod 4
+                    constexpr int W = BITS / 4;                          // words per chunk
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        uint32_t v[8];
+                        const int by = t == 0 ? 2 : 1;
+                        const bool on = (rot & by) != 0;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < W; ++e) v[c * W + e] = on ? u[((c + by) & 3) * W + e] : u[c * W + e];
+#pragma unroll
+                        for (int c = 0; c < 4 * W; ++c) u[c] = v[c];
+                    }
+                    ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
+                    if (!ok) break;
+                    const uint32_t line = as + ab * kPairABytes + (uint32_t)((q >> 1) * 8192 + r * 128);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        const int cc = (c + q) & 3;              // 16 channels 16·cc .. + 15
-                        const uint4 vv = lds128(row + (((4 * (q & 1) + cc) ^ (r & 7)) * 16));
+                        const int ch = 4 * (q & 1) + ((c + rot) & 3);
                         uint32_t d[4];
-                        pair_dequant8<8>(vv.x, vv.y, a.flip, cc < 2 ? z0 : z1, cc < 2 ? s0 : s1, d);
-                        sts128_addr(line + (uint32_t)(((2 * cc) ^ (r & 7)) * 16), d);
-                        pair_dequant8<8>(vv.z, vv.w, a.flip, cc < 2 ? z0 : z1, cc < 2 ? s0 : s1, d);
-                        sts128_addr(line + (uint32_t)(((2 * cc + 1) ^ (r & 7)) * 16), d);
+                        pair_dequant8<BITS>(u[c * W], u[c * W + W - 1], a.flip, zg, sg, d);
+                        sts128_addr(line + (uint32_t)((ch ^ (r & 7)) * 16), d);
                     }
+                    release();
+                    unit_done();
                 }
-                release(s, ab);
             }
-        }
-        // ------------------------------------------------------------ epilogue
-        if (ok && mbar_wait_cluster(smem_u32(accf), 0)) {
+            // -------------------------------------------------------- epilogue
+            if (!ok || !mbar_wait_cluster(accf, (uint32_t)seg & 1u)) break;
+            ++seg;
             tc_fence_after();
-            const int r = (warp & 3) * 32 + lane, h = w >> 2;
-            const int row0 = pair_row<DGRAD>(r0, rank, 0, r), row1 = pair_row<DGRAD>(r0, rank, 1, r);
-            const uint32_t t_lane = tmem_d + ((uint32_t)((warp & 3) * 32) << 16);
-            float* part = a.partials == nullptr ? nullptr
-                          : a.partials + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (2 * Cfg::kMmaN * kPairRows);
-#pragma unroll 1
-            for (int cb = h; cb < Cfg::kMmaN / 32; cb += 2) {
-                uint32_t v0[32], v1[32];
-                tmem_ld_32x32b_x32(t_lane + cb * 32, v0);
-                tmem_ld_32x32b_x32(t_lane + Cfg::kMmaN + cb * 32, v1);
+            const int quarter = warp & 3;                      // the lanes this warp may read
+            const int m0 = walk.tile % a.tiles_m * mma_n;
+            const int strips = (min(mma_n, a.M - m0) + 15) / 16;
+            const uint32_t t_lane = tmem_d + ((uint32_t)(quarter * 32) << 16);
+            // which of the quarter's four warps this one is
+            for (int sidx = w >> 2; sidx < strips; sidx += kPairDequantWarps / 4) {
+                uint32_t v0[16], v1[16];
+                const uint32_t t0 = t_lane + 16 * sidx;
+                tmem_ld_16x256b_x2(t0, v0);
+                tmem_ld_16x256b_x2(t0 + (16u << 16), v0 + 8);
+                tmem_ld_16x256b_x2(t0 + a.acc_cols, v1);
+                tmem_ld_16x256b_x2(t0 + a.acc_cols + (16u << 16), v1 + 8);
                 tmem_wait_ld();
-                if (part != nullptr) {
+                if (walk.part < 0) {
+                    float f0[16], f1[16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        part[(cb * 32 + j) * kPairRows + r] = __uint_as_float(v0[j]);
-                        part[(Cfg::kMmaN + cb * 32 + j) * kPairRows + r] = __uint_as_float(v1[j]);
+                    for (int e = 0; e < 16; ++e) {
+                        f0[e] = __uint_as_float(v0[e]);
+                        f1[e] = __uint_as_float(v1[e]);
                     }
+                    pair_emit<DGRAD>(a, f0, f1, st + w * 1024, r0, rank, quarter, m0 + 16 * sidx, lane);
                 } else {
+                    float4* part = reinterpret_cast<float4*>(
+                        a.partials + ((int64_t)(slot * 2 + walk.part) * kCtas + rank) * pair_part_floats(mma_n) +
+                        (int64_t)(sidx * 4 + quarter) * (2 * 16 * 32));
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int m = m0 + cb * 32 + j;
-                        if (m < a.M) pair_store<DGRAD>(a, row0, row1, m, __uint_as_float(v0[j]), __uint_as_float(v1[j]));
+                    for (int e = 0; e < 4; ++e) {
+                        part[e * 32 + lane] = make_float4(__uint_as_float(v0[4 * e]), __uint_as_float(v0[4 * e + 1]),
+                                                          __uint_as_float(v0[4 * e + 2]), __uint_as_float(v0[4 * e + 3]));
+                        part[(4 + e) * 32 + lane] =
+                            make_float4(__uint_as_float(v1[4 * e]), __uint_as_float(v1[4 * e + 1]),
+                                        __uint_as_float(v1[4 * e + 2]), __uint_as_float(v1[4 * e + 3]));
                     }
                 }
             }
+            tc_fence_before();      // the reads above precede this warp's next arrival, hence the next MMA
         }
+        __syncwarp();
     }
     tc_fence_before();
     __syncwarp();
+    __syncthreads();
     if constexpr (PAIR) cluster_sync_all();      // neither CTA leaves while the other may still use it
-    else __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_g<PAIR>(tmem_d, Cfg::kTmemCols);
+        tmem_dealloc_g<PAIR>(tmem_d, 2 * a.acc_cols);
     }
 }
 
-// Adds the parts of a split reduction in split order and runs the epilogue.  Parts are
-// [split][CTA][accumulator][token of the tile][128 rows]; one thread per row and token.
+// Adds the parts of the split tiles in the order of the reduction and runs the epilogue:
+// one warp per strip of a CTA's rows, in the layout the parts were left in.
+constexpr int kPairReduceThreads = 128;
 template <bool DGRAD>
-__global__ void __launch_bounds__(256) pair_reduce_kernel(const PairArgs a, int splits, int ctas, int mma_n,
-                                                          int kctas) {
+__global__ void __launch_bounds__(kPairReduceThreads) pair_reduce_kernel(const PairArgs a, int ctas, int upt) {
+    __shared__ __align__(16) uint8_t stage[kPairReduceThreads / 32 * 1024];
     grid_dependency_wait();
-    const int64_t per_cta = 2ll * mma_n * kPairRows;
-    const int64_t stride = (int64_t)ctas * per_cta;
-    const int64_t items = (int64_t)ctas * mma_n * kPairRows;
-    const int tiles_m = (a.M + mma_n - 1) / mma_n;
-    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < items;
-         e += (int64_t)gridDim.x * blockDim.x) {
-        const int cta = (int)(e / (mma_n * kPairRows));
-        const int in = (int)(e - (int64_t)cta * mma_n * kPairRows);
-        const int r = in % kPairRows, t = in / kPairRows;
-        const int tile = cta / kctas, rank = cta % kctas;
-        const int m = (tile % tiles_m) * mma_n + t;
-        if (m >= a.M) continue;
-        const int r0 = (tile / tiles_m) * (DGRAD ? 2 : 1) * kctas * kPairRows;
-        const float* p = a.partials + cta * per_cta + in;
-        float v0 = 0.0f, v1 = 0.0f;
-        for (int z = 0; z < splits; ++z) {
-            v0 += __ldcg(p + z * stride);
-            v1 += __ldcg(p + z * stride + (int64_t)mma_n * kPairRows);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int mma_n = ctas * a.bt, strips = (mma_n + 15) / 16;
+    const int64_t item = (int64_t)blockIdx.x * (kPairReduceThreads / 32) + warp;
+    const int quarter = (int)(item % 4), sidx = (int)(item / 4 % strips);
+    const int64_t rest = item / 4 / strips;
+    const int rank = (int)(rest % ctas), split = (int)(rest / ctas);
+    const int tile = a.whole + split;
+    if (tile >= a.tiles) return;
+    const int m = tile % a.tiles_m * mma_n + 16 * sidx;
+    if (m >= a.M) return;
+    const int64_t total = (int64_t)(a.tiles - a.whole) * upt, u0 = (int64_t)split * upt, u1 = u0 + upt;
+    // sharer c holds units [total·c/S, total·(c + 1)/S)
+    const int first = (int)(((u0 + 1) * a.sharers - 1) / total), last = (int)((u1 * a.sharers - 1) / total);
+    float v0[16], v1[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v0[e] = v1[e] = 0.0f;
+    for (int c = first; c <= last; ++c) {
+        const int seg = total * c / a.sharers >= u0 ? 0 : 1;       // the tile is the sharer's first or second
+        const float4* part = reinterpret_cast<const float4*>(
+            a.partials + ((int64_t)(c * 2 + seg) * ctas + rank) * pair_part_floats(mma_n) +
+            (int64_t)(sidx * 4 + quarter) * (2 * 16 * 32));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float4 p = __ldcg(part + e * 32 + lane), q = __ldcg(part + (4 + e) * 32 + lane);
+            v0[4 * e] += p.x; v0[4 * e + 1] += p.y; v0[4 * e + 2] += p.z; v0[4 * e + 3] += p.w;
+            v1[4 * e] += q.x; v1[4 * e + 1] += q.y; v1[4 * e + 2] += q.z; v1[4 * e + 3] += q.w;
         }
-        pair_store<DGRAD>(a, pair_row<DGRAD>(r0, rank, 0, r), pair_row<DGRAD>(r0, rank, 1, r), m, v0, v1);
     }
+    pair_emit<DGRAD>(a, v0, v1, smem_u32(stage) + warp * 1024, pair_row0<DGRAD>(a, tile, ctas), rank, quarter, m, lane);
 }
 
 }  // namespace w4a16

@@ -60,55 +60,106 @@ w4a16_status set_smem(F* kern, int bytes, bool (&done)[kMaxDevices]) {
 }
 
 // ---------------------------------------------------------------- gemm_pair launches
-// Launch of the tensor-core kernels: tokens per tile, CTAs per tile, tiles and the split
-// of the reduction.  Split only when the tiles leave half of the SMs without one: the
-// parts (binary32, both accumulators) are then written and read once more.
+// Launch of the tensor-core kernels (host copy of what the kernel derives its work from).
 struct PairPlan {
     int bt;            // tokens of a CTA's tile
     int ctas;          // 1, or 2 for a pair
+    int blocks;        // reduction blocks of 64 per tile
+    int upt;           // code units per tile
+    int tiles_m;
     int64_t tiles;
-    int blocks;        // reduction blocks of 64
-    int splits;
-    int blocks_split;
+    int64_t whole;     // tiles computed whole
+    int sharers;       // CTAs (pairs) that share the others
+    int grid;          // CTAs (pairs) launched
     int64_t bytes;     // workspace of the parts
 };
 
-PairPlan pair_plan(int64_t M, int64_t rows, int rows_per_cta, int64_t blocks, int sm_count) {
+// `rows` output rows (features or input channels) in tiles of `rows_per_cta` per CTA.
+//
+// Token tile: the batch in equal tiles of at most 128 tokens for one CTA (one tile) and
+// 256 for a pair, in steps of 16.
+//
+// Split: whole waves of tiles are dealt as they are.  The rest leaves CTAs without work;
+// splitting it over all of them along the reduction saves the idle share of a tile's time
+// and costs writing and reading binary32 parts and a second kernel.  Both sides are
+// estimated and the smaller taken: a block takes about 0.55 us per 256 tokens, at least
+// 0.25 us (dequantization); parts move at about 3 TB/s, the second kernel takes 3 us.
+PairPlan pair_plan(int64_t M, int64_t rows, int rows_per_cta, int64_t blocks, int unit_blocks, int sm_count) {
     PairPlan p{};
-    p.bt = M <= 32 ? 32 : (M <= 64 ? 64 : 128);
     p.ctas = M > 128 ? 2 : 1;
-    const int64_t tokens = (int64_t)p.bt * p.ctas;
-    p.tiles = ((M + tokens - 1) / tokens) * ((rows + rows_per_cta * p.ctas - 1) / (rows_per_cta * p.ctas));
+    const int64_t most = p.ctas == 2 ? 256 : 128;
+    const int64_t tiles_m = (M + most - 1) / most;
+    const int64_t tokens = ((M + tiles_m - 1) / tiles_m + 15) / 16 * 16;
+    p.bt = (int)(tokens / p.ctas);
+    p.tiles_m = (int)tiles_m;
+    p.tiles = tiles_m * ((rows + rows_per_cta * p.ctas - 1) / (rows_per_cta * p.ctas));
     p.blocks = (int)blocks;
+    p.upt = (int)((blocks + unit_blocks - 1) / unit_blocks);
     const int64_t slots = sm_count / p.ctas;
-    int64_t s = p.tiles > 0 ? slots / p.tiles : 1;
-    if (s > blocks / 4) s = blocks / 4;
-    if (s > 16) s = 16;
-    if (s < 1) s = 1;
-    p.blocks_split = (int)((blocks + s - 1) / s);
-    p.splits = p.blocks_split > 0 ? (int)((blocks + p.blocks_split - 1) / p.blocks_split) : 1;
-    if (p.splits > 1)
-        p.bytes = (int64_t)p.splits * p.tiles * p.ctas * 2 * tokens * kPairRows * 4;
+    p.whole = p.tiles / slots * slots;
+    const int64_t rest = p.tiles - p.whole;
+    if (rest > 0) {
+        const int64_t part = pair_part_floats((int)tokens) * 4 * p.ctas;
+        // at least two units of work for each sharer
+        int64_t sharers = rest * p.upt / 2;
+        if (sharers > slots) sharers = slots;
+        const double block_us = tokens * 0.55 / 256 > 0.25 ? tokens * 0.55 / 256 : 0.25;
+        const double saved = blocks * block_us * (1.0 - (double)rest / (double)sharers);
+        const double paid = 3.0 + 2.0 * (double)((rest + sharers) * part) / 3e6;
+        if (sharers > rest && saved > paid) {
+            p.sharers = (int)sharers;
+            p.bytes = sharers * 2 * part;
+        } else {
+            p.whole = p.tiles;
+        }
+    }
+    p.grid = (int)(p.whole < slots ? p.whole : slots);
+    if (p.sharers > p.grid) p.grid = p.sharers;
     return p;
 }
 
-template <int BT, bool PAIR, int BITS, bool DGRAD>
+template <typename... A, typename... B>
+w4a16_status launch_chained(void (*kern)(A...), dim3 grid, int threads, cudaStream_t stream, B... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, static_cast<A>(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return W4A16_ECUDA;
+    }
+    return W4A16_OK;
+}
+
+template <bool PAIR, int BITS, bool DGRAD>
 w4a16_status launch_pair_t(const PairPlan& p, const CUtensorMap* tmX, const CUtensorMap* tmP, PairArgs args,
                            cudaStream_t stream) {
-    using Cfg = PairConfig<BT, PAIR, BITS>;
-    auto kern = gemm_pair_kernel<BT, PAIR, BITS, DGRAD>;
+    auto kern = gemm_pair_kernel<PAIR, BITS, DGRAD>;
     static bool done[kMaxDevices] = {};
-    w4a16_status st = set_smem(kern, Cfg::kSmemBytes, done);
+    w4a16_status st = set_smem(kern, kPairSmemBytes, done);
     if (st != W4A16_OK) return st;
+    args.bt = p.bt;
+    args.acc_cols = 32;
+    while (args.acc_cols < p.bt * p.ctas) args.acc_cols *= 2;
+    args.blocks = p.blocks;
+    args.tiles_m = p.tiles_m;
+    args.whole = (int)p.whole;
+    args.tiles = (int)p.tiles;
+    args.sharers = p.sharers;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.tiles * p.ctas), (unsigned)p.splits, 1);
+    cfg.gridDim = dim3((unsigned)(p.grid * p.ctas), 1, 1);
     cfg.blockDim = dim3(kPairThreads, 1, 1);
-    cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+    cfg.dynamicSmemBytes = kPairSmemBytes;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 1 : 0;
@@ -116,21 +167,19 @@ w4a16_status launch_pair_t(const PairPlan& p, const CUtensorMap* tmX, const CUte
         cudaGetLastError();
         return W4A16_ECUDA;
     }
-    if (p.splits > 1) {
-        const int64_t items = p.tiles * p.ctas * Cfg::kMmaN * (int64_t)kPairRows;
-        pair_reduce_kernel<DGRAD><<<grid_for(items, 256, current_sm_count()), 256, 0, stream>>>(
-            args, p.splits, (int)(p.tiles * p.ctas), Cfg::kMmaN, p.ctas);
-    }
-    return launch_status();
+    if (p.sharers == 0) return W4A16_OK;
+    const int64_t warps = (p.tiles - p.whole) * p.ctas * ((p.bt * p.ctas + 15) / 16) * 4;
+    const int per = kPairReduceThreads / 32;
+    return launch_chained(pair_reduce_kernel<DGRAD>, dim3((unsigned)((warps + per - 1) / per)), kPairReduceThreads,
+                          stream, args, p.ctas, p.upt);
 }
 
 template <int BITS, bool DGRAD>
 w4a16_status launch_pair(const PairPlan& p, const CUtensorMap* tmX, const CUtensorMap* tmP, const PairArgs& args,
                          cudaStream_t stream) {
-    if (p.ctas == 2) return launch_pair_t<128, true, BITS, DGRAD>(p, tmX, tmP, args, stream);
-    if (p.bt == 32) return launch_pair_t<32, false, BITS, DGRAD>(p, tmX, tmP, args, stream);
-    if (p.bt == 64) return launch_pair_t<64, false, BITS, DGRAD>(p, tmX, tmP, args, stream);
-    return launch_pair_t<128, false, BITS, DGRAD>(p, tmX, tmP, args, stream);
+    if (p.tiles > kMaxDim) return W4A16_EINVAL;
+    return p.ctas == 2 ? launch_pair_t<true, BITS, DGRAD>(p, tmX, tmP, args, stream)
+                       : launch_pair_t<false, BITS, DGRAD>(p, tmX, tmP, args, stream);
 }
 
 struct Weights {
@@ -174,18 +223,17 @@ w4a16_status launch_dgrad(const PairPlan& p, const void* const* dY, const Weight
     PairArgs a{};
     fill_weight_args(&a, w, products, K, g, sym, bits);
     a.out = static_cast<uint16_t*>(dX);
-    a.partials = p.splits > 1 ? static_cast<float*>(parts) : nullptr;
+    a.partials = static_cast<float*>(parts);
     a.M = (int)M;
     a.N = (int)N;
     a.K = (int)K;
     a.products = products;
-    a.blocks = p.blocks;
-    a.blocks_split = p.blocks_split;
     return bits == 8 ? launch_pair<8, true>(p, tmX, tmP, a, stream) : launch_pair<4, true>(p, tmX, tmP, a, stream);
 }
 
 PairPlan dgrad_plan(int64_t M, int64_t N, int64_t K, int products) {
-    return pair_plan(M, K, 2 * kPairRows, (int64_t)products * ((N + kPairBlock - 1) / kPairBlock), current_sm_count());
+    return pair_plan(M, K, 2 * kPairRows, (int64_t)products * ((N + kPairBlock - 1) / kPairBlock), 1,
+                     current_sm_count());
 }
 
 // ---------------------------------------------------------------- gated, decode form
@@ -247,7 +295,7 @@ w4a16_status gated_plan(int64_t M, int64_t N, int64_t K, int32_t g, int32_t path
         if (q.grid < 1) q.grid = 1;
         q.bytes = decode_workspace_bytes(q.d, q.grid);
     } else {
-        q.p = pair_plan(M, N, kPairRows, (K + kPairBlock - 1) / kPairBlock, current_sm_count());
+        q.p = pair_plan(M, N, kPairRows, (K + kPairBlock - 1) / kPairBlock, bits == 4 ? 2 : 1, current_sm_count());
         q.bytes = q.p.bytes;
     }
     *out = q;
@@ -348,8 +396,7 @@ w4a16_status gated_impl(const void* X, int64_t M, int64_t K, const Weights* w, i
     const uint64_t row_bytes = (uint64_t)K * bits / 8;
     for (int i = 0; i < 2; ++i) {
         st = encode_rows(&tmP[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w[i].codes, row_bytes, (uint64_t)N, row_bytes,
-                         (uint32_t)(kPairBlock * bits / 8), kPairRows,
-                         bits == 8 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+                         64, kPairRows, CU_TENSOR_MAP_SWIZZLE_64B);
         if (st != W4A16_OK) return st;
     }
     PairArgs a{};
@@ -357,14 +404,12 @@ w4a16_status gated_impl(const void* X, int64_t M, int64_t K, const Weights* w, i
     a.out = static_cast<uint16_t*>(H);
     a.G = static_cast<uint16_t*>(G);
     a.U = static_cast<uint16_t*>(U);
-    a.partials = q.p.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+    a.partials = static_cast<float*>(workspace);
     a.M = (int)M;
     a.N = (int)N;
     a.K = (int)K;
     a.act = act;
     a.products = 1;
-    a.blocks = q.p.blocks;
-    a.blocks_split = q.p.blocks_split;
     return bits == 8 ? launch_pair<8, false>(q.p, tmX, tmP, a, s) : launch_pair<4, false>(q.p, tmX, tmP, a, s);
 }
 
@@ -499,24 +544,6 @@ EmbedGradPlan embed_grad_plan(int64_t T, int64_t K) {
 
 bool embed_grad_ok(int64_t T, int64_t V, int64_t K) {
     return T >= 0 && V >= 0 && K > 0 && K % 32 == 0 && T <= kMaxDim / 2 && V < kMaxDim && K <= kMaxDim;
-}
-
-template <typename... A, typename... B>
-w4a16_status launch_chained(void (*kern)(A...), dim3 grid, int threads, cudaStream_t stream, B... args) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, kern, static_cast<A>(args)...) != cudaSuccess) {
-        cudaGetLastError();
-        return W4A16_ECUDA;
-    }
-    return W4A16_OK;
 }
 
 template <bool F32>

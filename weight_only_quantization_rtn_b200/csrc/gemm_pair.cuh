@@ -256,13 +256,12 @@ struct PairWalk {
     }
 };
 
-// Zero point as the dequantization wants it: the bf16 pair of 128 + z (4-bit codes), or
-// the binary32 2^23 + z (8-bit codes).
+// Zero point as the dequantization wants it, from the bf16 pair (z, z): the pair of
+// 128 + z (4-bit codes), or the binary32 2^23 + z (8-bit codes).
 template <int BITS>
-__device__ __forceinline__ uint32_t pair_zero(uint32_t z_bits, bool sym, float zsym) {
-    const float z = sym ? zsym : bf16_bits_to_f32(z_bits);
-    if (BITS == 4) return dup16(f32_to_bf16_bits_rn(128.0f + z));
-    return __float_as_uint(8388608.0f + z);
+__device__ __forceinline__ uint32_t pair_zero(uint32_t zz, bool sym, float zsym) {
+    if (BITS == 4) return sym ? 0x43084308u : bf16x2_add(zz, 0x43004300u);
+    return __float_as_uint(8388608.0f + (sym ? zsym : __uint_as_float(zz & 0xFFFF0000u)));
 }
 
 // Eight codes -> four bf16 pairs in natural order.  4 bits (w0): PRMT brings code 2j of
@@ -271,9 +270,9 @@ __device__ __forceinline__ uint32_t pair_zero(uint32_t z_bits, bool sym, float z
 // the same LOP3).  8 bits (w0, w1): as dequant4_bytes in gemm_tcgen05.cuh.
 template <int BITS>
 __device__ __forceinline__ void pair_dequant8(uint32_t w0, uint32_t w1, uint32_t flip, uint32_t zz,
-                                              uint32_t s_bits, uint32_t out[4]) {
+                                              uint32_t ss, uint32_t out[4]) {
     if constexpr (BITS == 4) {
-        const uint32_t ss = dup16(s_bits), magic = 0x43004300u | (flip & 0x00080008u), hi = w0 >> 4;
+        const uint32_t magic = 0x43004300u | (flip & 0x00080008u), hi = w0 >> 4;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             // bytes: [w.j, any, (w >> 4).j, any]
@@ -283,7 +282,7 @@ __device__ __forceinline__ void pair_dequant8(uint32_t w0, uint32_t w1, uint32_t
             out[j] = bf16x2_mul(bf16x2_sub(q, zz), ss);
         }
     } else {
-        const float s = bf16_bits_to_f32(s_bits), zoff = __uint_as_float(zz);
+        const float s = __uint_as_float(ss & 0xFFFF0000u), zoff = __uint_as_float(zz);
         const uint32_t w[2] = {w0 ^ flip, w1 ^ flip};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -384,8 +383,17 @@ __device__ __forceinline__ void pair_emit(const PairArgs& a, float v0[16], float
             strip_store(v0, stage, a.G, m, a.M, c, a.N, lane);
             strip_store(v1, stage, a.U, m, a.M, c, a.N, lane);
         }
+        // (the choice of the activation outside the loop)
+        if (a.act == W4A16_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v0[i] = act_value(a.act, v0[i]) * v1[i];
+            for (int i = 0; i < 16; ++i) v0[i] = act_value(W4A16_ACT_SILU, v0[i]) * v1[i];
+        } else if (a.act == W4A16_ACT_GELU) {
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i) v0[i] = act_value(W4A16_ACT_GELU, v0[i]) * v1[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v0[i] = act_value(a.act, v0[i]) * v1[i];
+        }
         strip_store(v0, stage, a.out, m, a.M, c, a.N, lane);
     }
 }
@@ -439,10 +447,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         for (int s = 0; s < SP; ++s) {
             mbar_init(pfull + 8 * s, 1);
-            mbar_init(pempty + 8 * s, kPairDequantWarps);
+            mbar_init(pempty + 8 * s, UB * kPairDequantWarps / 2);
         }
         for (int s = 0; s < NA; ++s) {
-            mbar_init(afull + 8 * s, kCtas * kPairDequantWarps);
+            mbar_init(afull + 8 * s, kCtas * kPairDequantWarps / 2);
             mbar_init(aempty + 8 * s, 1);
         }
         mbar_init(accf, 1);
@@ -570,202 +578,215 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------------ dequantize, epilogue
-        const int w = warp - 2;
+        // Two groups of eight warps take the blocks in turn, so that one group's waits, fences
+        // and loads hide behind the other's arithmetic and each warp pays its per-block
+        // overhead for eight chunks of codes.
+        const int w = warp - 2, grp = w >> 3, wg = w & 7;
         const bool sym = a.flip != 0u;
         const uint32_t afull_r = PAIR ? mapa_u32(afull, 0) : afull;
-        int xslot = 0, ab = 0, pslot = 0, seg = 0;
-        uint32_t xph = 0, aph = 0, pph = 0;
+        int cnt = 0, ucnt = 0, seg = 0;              // blocks and units of the segments before
         bool ok = true;
-        // The A tiles of a block are written: visible to the tensor core, then counted.
-        auto release = [&]() {
-            fence_proxy_async_smem();
-            __syncwarp();
-            // one warp per CTA also vouches for the block's tokens
-            if (w == 0) ok = mbar_wait(xfull + 8 * xslot, xph) && ok;
-            if (lane == 0) {
-                if constexpr (PAIR) mbar_arrive_cluster(afull_r + 8 * ab);
-                else mbar_arrive(afull_r + 8 * ab);
-            }
-            if (++xslot == SX) { xslot = 0; xph ^= 1u; }
-            if (++ab == NA) { ab = 0; aph ^= 1u; }
-        };
-        // The next unit's codes are read from the slot behind; a slot is given back only once
-        // the codes were used.  (Given back right behind the loads, a slot was seen refilled
-        // before a load of it had been performed: the load's value is needed first.)
-        int pdone = 0;
-        auto unit_next = [&]() {
-            if (++pslot == SP) { pslot = 0; pph ^= 1u; }
-        };
-        auto unit_done = [&]() {                 // behind release(): all lanes used their codes
-            if (lane == 0) mbar_arrive(pempty + 8 * pdone);
-            if (++pdone == SP) pdone = 0;
-        };
         while (ok && walk.next(a)) {
             const int r0 = pair_row0<DGRAD>(a, walk.tile, kCtas);
             const int b0 = walk.first_block(), nb = walk.count(a);
+            // this group's first block in each ring: slot and phase
+            int ab = (cnt + grp) % NA, xslot = (cnt + grp) % SX;
+            uint32_t aph = (uint32_t)((cnt + grp) / NA) & 1u, xph = (uint32_t)((cnt + grp) / SX) & 1u;
+            const int ufirst = ucnt + (UB == 2 ? 0 : grp);
+            int pslot = ufirst % SP;
+            uint32_t pph = (uint32_t)(ufirst / SP) & 1u;
+            cnt += nb;
+            ucnt += walk.units;
+            // The A tiles of a block are written: visible to the tensor core, then counted; the
+            // codes were used, so their slot is given back.  (Given back right behind the
+            // loads, a slot was seen refilled before a load of it had been performed.)
+            auto release = [&]() {
+                fence_proxy_async_smem();
+                __syncwarp();
+                // one warp of the group also vouches for the block's tokens
+                if (wg == 0) ok = mbar_wait(xfull + 8 * xslot, xph) && ok;
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_cluster(afull_r + 8 * ab);
+                    else mbar_arrive(afull + 8 * ab);
+                    mbar_arrive(pempty + 8 * pslot);
+                }
+                xslot += 2;
+                if (xslot >= SX) { xslot -= SX; xph ^= 1u; }
+                ab += 2;
+                if (ab >= NA) { ab -= NA; aph ^= 1u; }
+                pslot += UB == 2 ? 1 : 2;
+                if (pslot >= SP) { pslot -= SP; pph ^= 1u; }
+            };
             if constexpr (!DGRAD) {
-                // thread = row r of matrix j, 32-wide half h of the block
-                const int j = w >> 3, r = (w & 3) * 32 + lane, h = (w >> 2) & 1;
+                // thread = row r of both matrices, 32-wide half h of the block
+                const int r = (wg & 3) * 32 + lane, h = wg >> 2;
                 const int n = r0 + rank * kPairRows + r;
                 const bool row_ok = n < a.N;
                 const bool vec = (a.groups & 7) == 0;         // rows of scales are 16-byte aligned
-                const uint16_t* sp = (j ? a.scales[1] : a.scales[0]) + (int64_t)(row_ok ? n : 0) * a.groups;
-                const uint16_t* zp = (sym ? sp : (j ? a.zeros[1] : a.zeros[0]) + (int64_t)(row_ok ? n : 0) * a.groups);
-                // the eight groups around the current one, and the next eight
-                uint4 sv = make_uint4(0, 0, 0, 0), zv = sv, sn = sv, zn = sv;
+                const int64_t srow = (int64_t)(row_ok ? n : 0) * a.groups;
+                const uint32_t sts0 = (uint32_t)(r * 128 + (((4 * h) ^ (r & 7)) * 16));   // chunk c: ^ 16·c
+                const uint32_t lds0 = ps + (uint32_t)(r * 64) +
+                                      (uint32_t)(((BITS == 4 ? 2 * grp + h : 2 * h) ^ ((r >> 1) & 3)) * 16);
+                uint32_t ss[2], zz[2];                        // the current group's pairs
                 int have = -1;
-                uint32_t sg = 0u, zg = 0u, sraw = 0u, zraw = 0u;
-                auto slab = [&](int grp, uint4& s8, uint4& z8) {
-                    if (row_ok && grp < a.groups) {
-                        s8 = ldg_cached(sp + grp);
-                        if (!sym) z8 = ldg_cached(zp + grp);
+                if (!vec) {
+                    // the pair of the group ahead, loaded one change early
+                    const int g0 = min(((b0 + grp) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        ss[j] = row_ok ? ldg_u16(a.scales[j] + srow + g0) : 0u;
+                        zz[j] = row_ok && !sym ? ldg_u16(a.zeros[j] + srow + g0) : 0u;
                     }
-                };
-                auto single = [&](int grp) {
-                    if (row_ok && grp < a.groups) {
-                        sraw = ldg_u16(sp + grp);
-                        if (!sym) zraw = ldg_u16(zp + grp);
-                    }
-                };
-                {
-                    const int g0 = min((b0 * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
-                    if (vec) slab(g0 & ~7, sn, zn);
-                    else single(g0);
                 }
-                auto scales_of = [&](int i) {
-                    const int grp = min(((b0 + i) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
-                    if (grp == have) return;
-                    uint32_t sb, zb;
-                    if (vec) {
-                        if (have < 0 || (grp >> 3) != (have >> 3)) {
-                            sv = sn;
-                            zv = zn;
-                            slab((grp & ~7) + 8, sn, zn);
+                uint4 s8[2], z8[2];                           // eight groups of the row
+                uint32_t sc[2] = {0u, 0u}, zc[2] = {0u, 0u};
+                for (int i = grp; i < nb && ok; i += 2) {
+                    const int g = min(((b0 + i) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
+                    if (g != have) {
+                        if (vec) {
+                            if (have < 0 || (g >> 3) != (have >> 3)) {
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    s8[j] = row_ok ? ldg_cached(a.scales[j] + srow + (g & ~7)) : make_uint4(0, 0, 0, 0);
+                                    z8[j] = row_ok && !sym ? ldg_cached(a.zeros[j] + srow + (g & ~7)) : make_uint4(0, 0, 0, 0);
+                                }
+                            }
+                            const bool up = (g & 4) != 0, odd = (g & 2) != 0;
+                            const uint32_t sel = (g & 1) ? 0x3232u : 0x1010u;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t s0 = up ? s8[j].z : s8[j].x, s1 = up ? s8[j].w : s8[j].y;
+                                const uint32_t z0 = up ? z8[j].z : z8[j].x, z1 = up ? z8[j].w : z8[j].y;
+                                sc[j] = __byte_perm(odd ? s1 : s0, 0u, sel);
+                                zc[j] = pair_zero<BITS>(__byte_perm(odd ? z1 : z0, 0u, sel), sym, a.zsym);
+                            }
+                        } else {
+                            const int gn = min(((b0 + i + 2) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
+                            const int ahead = gn != g ? gn : min(g + 1, a.groups - 1);
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                sc[j] = dup16(ss[j]);
+                                zc[j] = pair_zero<BITS>(dup16(zz[j]), sym, a.zsym);
+                                ss[j] = row_ok ? ldg_u16(a.scales[j] + srow + ahead) : 0u;
+                                zz[j] = row_ok && !sym ? ldg_u16(a.zeros[j] + srow + ahead) : 0u;
+                            }
                         }
-                        const int q = grp & 7;
-                        const uint32_t sw = q < 4 ? (q < 2 ? sv.x : sv.y) : (q < 6 ? sv.z : sv.w);
-                        const uint32_t zw = q < 4 ? (q < 2 ? zv.x : zv.y) : (q < 6 ? zv.z : zv.w);
-                        sb = (sw >> (16 * (q & 1))) & 0xFFFFu;
-                        zb = (zw >> (16 * (q & 1))) & 0xFFFFu;
-                    } else {
-                        sb = sraw;
-                        zb = zraw;
-                        single(((b0 + i + 1) * kPairBlock + 32 * h) >> a.gshift == grp
-                                   ? grp + 1
-                                   : min(((b0 + i + 1) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1));
+                        have = g;
                     }
-                    sg = sb;
-                    zg = pair_zero<BITS>(zb, sym, a.zsym);
-                    have = grp;
-                };
-                constexpr int kRowBytes = kPairBlock * UB * BITS / 8;      // 64
-                uint4 c0v, c1v = make_uint4(0, 0, 0, 0);
-                auto codes_of = [&](int i) {
-                    if (i % UB == 0) ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
-                    const uint32_t row = ps + pslot * Unit::kBytes + j * (Unit::kBytes / 2) + r * kRowBytes;
-                    if constexpr (BITS == 4) {
-                        c0v = lds128_addr(row + (uint32_t)(((2 * (i % UB) + h) ^ ((r >> 1) & 3)) * 16));
-                    } else {
-                        c0v = lds128_addr(row + (uint32_t)(((2 * h) ^ ((r >> 1) & 3)) * 16));
-                        c1v = lds128_addr(row + (uint32_t)(((2 * h + 1) ^ ((r >> 1) & 3)) * 16));
+                    ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
+                    uint4 v[2], v8[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t at = lds0 + (uint32_t)(pslot * Unit::kBytes + j * (Unit::kBytes / 2));
+                        v[j] = lds128_addr(at);
+                        v8[j] = BITS == 8 ? lds128_addr(at ^ 16u) : make_uint4(0, 0, 0, 0);
                     }
-                    if (i % UB == UB - 1 || i == nb - 1) unit_next();
-                };
-                codes_of(0);
-                for (int i = 0; i < nb && ok; ++i) {
-                    const uint32_t wv[8] = {c0v.x, c0v.y, c0v.z, c0v.w, c1v.x, c1v.y, c1v.z, c1v.w};
-                    scales_of(i);
-                    if (i + 1 < nb) codes_of(i + 1);
                     ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
                     if (!ok) break;
-                    const uint32_t arow = as + ab * kPairABytes + j * (kPairABytes / 2) + r * 128;
+                    const uint32_t arow = as + (uint32_t)(ab * kPairABytes) + sts0;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t d[4];
-                        if constexpr (BITS == 4) pair_dequant8<4>(wv[c], 0u, a.flip, zg, sg, d);
-                        else pair_dequant8<8>(wv[2 * c], wv[2 * c + 1], a.flip, zg, sg, d);
-                        sts128_addr(arow + (uint32_t)(((4 * h + c) ^ (r & 7)) * 16), d);
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t wv[8] = {v[j].x, v[j].y, v[j].z, v[j].w, v8[j].x, v8[j].y, v8[j].z, v8[j].w};
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t d[4];
+                            if constexpr (BITS == 4) pair_dequant8<4>(wv[c], 0u, a.flip, zc[j], sc[j], d);
+                            else pair_dequant8<8>(wv[2 * c], wv[2 * c + 1], a.flip, zc[j], sc[j], d);
+                            sts128_addr((arow ^ (uint32_t)(16 * c)) + (uint32_t)(j * (kPairABytes / 2)), d);
+                        }
                     }
                     release();
-                    if (i % UB == UB - 1 || i == nb - 1) unit_done();
+                }
+                if (UB == 2 && ok && grp == 1 && (nb & 1)) {
+                    // the segment's last unit has no block for this group
+                    ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
+                    if (lane == 0) mbar_arrive(pempty + 8 * pslot);
                 }
             } else {
-                // thread = weight row r of the block, 32-channel piece q: the eight threads of a
-                // row are neighbours, so that a warp's scale loads touch four rows.  Those that
-                // store into the same banks (64 channels apart) take their four chunks in
-                // rotated order.
-                const int r = w * 4 + (lane >> 3), q = lane & 7, rot = q >> 1;
-                const int c0 = r0 + rank * 2 * kPairRows + 32 * q;       // first input channel
+                // thread = weight row r of the block, 64-channel block q: the four threads of a row
+                // are neighbours, so that a warp's scale loads touch eight rows.  Each starts
+                // at another chunk (2q), which keeps its shared-memory stores off the banks
+                // of the other three.
+                const int r = wg * 8 + (lane >> 2), q = lane & 3;
+                const int c0 = r0 + rank * 2 * kPairRows + 64 * q;       // first input channel
                 const bool chan_ok = c0 < a.K;
-                const int grp = min(c0 >> a.gshift, a.groups - 1);
-                auto fetch = [&](int i, uint32_t& sb, uint32_t& zb) {
-                    sb = zb = 0u;
+                const int g0 = min(c0 >> a.gshift, a.groups - 1), g1 = min((c0 + 32) >> a.gshift, a.groups - 1);
+                auto fetch = [&](int i, uint32_t* sb, uint32_t* zb) {
                     int b = b0 + i;
                     const bool second = b >= per_product;
                     if (second) b -= per_product;
                     const int n = b * kPairBlock + r;
+                    sb[0] = sb[1] = zb[0] = zb[1] = 0u;
                     if (i < nb && n < a.N && chan_ok) {
-                        const int64_t at = (int64_t)n * a.groups + grp;
-                        sb = ldg_u16((second ? a.scales[1] : a.scales[0]) + at);
-                        if (!sym) zb = ldg_u16((second ? a.zeros[1] : a.zeros[0]) + at);
+                        const uint16_t* sp = (second ? a.scales[1] : a.scales[0]) + (int64_t)n * a.groups;
+                        const uint16_t* zp = (second ? a.zeros[1] : a.zeros[0]) + (int64_t)n * a.groups;
+                        sb[0] = ldg_u16(sp + g0);
+                        if (!sym) zb[0] = ldg_u16(zp + g0);
+                        if (g1 != g0) {
+                            sb[1] = ldg_u16(sp + g1);
+                            if (!sym) zb[1] = ldg_u16(zp + g1);
+                        }
                     }
                 };
-                // pairs of the next three blocks
-                uint32_t s0, z0, s1, z1, s2, z2;
-                fetch(0, s0, z0);
-                fetch(1, s1, z1);
-                fetch(2, s2, z2);
-                uint4 c0v, c1v = make_uint4(0, 0, 0, 0);
-                auto codes_of = [&]() {
-                    ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
-                    const uint32_t row = ps + pslot * Unit::kBytes + r * 128;
-                    if constexpr (BITS == 4) {
-                        c0v = lds128_addr(row + (uint32_t)((q ^ (r & 7)) * 16));
-                    } else {
-                        // 32 bytes: chunks 2(q & 3), + 1 of box q / 4; the boxes read them in opposite order
-                        const uint32_t box = row + (uint32_t)(q >> 2) * (kPairBlock * 128);
-                        const int f = q >> 2;
-                        const uint4 e0 = lds128_addr(box + (uint32_t)(((2 * (q & 3) + f) ^ (r & 7)) * 16));
-                        const uint4 e1 = lds128_addr(box + (uint32_t)(((2 * (q & 3) + 1 - f) ^ (r & 7)) * 16));
-                        c0v = f ? e1 : e0;
-                        c1v = f ? e0 : e1;
-                    }
-                    unit_next();
-                };
-                codes_of();
-                for (int i = 0; i < nb && ok; ++i) {
-                    uint32_t u[8] = {c0v.x, c0v.y, c0v.z, c0v.w, c1v.x, c1v.y, c1v.z, c1v.w};
-                    const uint32_t sg = s0, zg = pair_zero<BITS>(z0, sym, a.zsym);
-                    s0 = s1; z0 = z1;
-                    s1 = s2; z1 = z2;
-                    fetch(i + 3, s2, z2);
-                    if (i + 1 < nb) codes_of();
-                    // chunk c of the rotated order is chunk (c + rot) mod 4
-                    constexpr int W = BITS / 4;                          // words per chunk
+                // pairs of this group's next two blocks
+                uint32_t sn[2][2], zn[2][2];
+                fetch(grp, sn[0], zn[0]);
+                fetch(grp + 2, sn[1], zn[1]);
+                const uint32_t row = ps + (uint32_t)(r * 128);
+                const uint32_t line = as + (uint32_t)(q * 8192 + r * 128);
+                for (int i = grp; i < nb && ok; i += 2) {
+                    uint32_t sc[2], zc[2];
+                    sc[0] = dup16(sn[0][0]);
+                    zc[0] = pair_zero<BITS>(dup16(zn[0][0]), sym, a.zsym);
+                    sc[1] = g1 != g0 ? dup16(sn[0][1]) : sc[0];
+                    zc[1] = g1 != g0 ? pair_zero<BITS>(dup16(zn[0][1]), sym, a.zsym) : zc[0];
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
-                        uint32_t v[8];
-                        const int by = t == 0 ? 2 : 1;
-                        const bool on = (rot & by) != 0;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < W; ++e) v[c * W + e] = on ? u[((c + by) & 3) * W + e] : u[c * W + e];
-#pragma unroll
-                        for (int c = 0; c < 4 * W; ++c) u[c] = v[c];
+                        sn[0][t] = sn[1][t];
+                        zn[0][t] = zn[1][t];
                     }
-                    ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
-                    if (!ok) break;
-                    const uint32_t line = as + ab * kPairABytes + (uint32_t)((q >> 1) * 8192 + r * 128);
+                    fetch(i + 4, sn[1], zn[1]);
+                    ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
+                    const uint32_t prow = row + (uint32_t)(pslot * Unit::kBytes);
+                    const uint32_t aline = line + (uint32_t)(ab * kPairABytes);
+                    if constexpr (BITS == 4) {
+                        // 32 code bytes: logical chunks 2q, 2q + 1 of the row's eight (128-byte swizzle)
+                        const uint32_t at = prow + (uint32_t)(((2 * q) ^ (r & 7)) * 16);
+                        const uint4 va = lds128_addr(at), vb = lds128_addr(at ^ 16u);
+                        uint32_t u[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w}, v[8];
+                        // u rotated by 2q words: step c handles chunk (c + 2q) mod 8
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int ch = 4 * (q & 1) + ((c + rot) & 3);
-                        uint32_t d[4];
-                        pair_dequant8<BITS>(u[c * W], u[c * W + W - 1], a.flip, zg, sg, d);
-                        sts128_addr(line + (uint32_t)((ch ^ (r & 7)) * 16), d);
+                        for (int c = 0; c < 8; ++c) v[c] = (q & 2) ? u[(c + 4) & 7] : u[c];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) u[c] = (q & 1) ? v[(c + 2) & 7] : v[c];
+                        ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
+                        if (!ok) break;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const int ch = (c + 2 * q) & 7;
+                            const bool hi = ch >= 4;
+                            uint32_t d[4];
+                            pair_dequant8<4>(u[c], 0u, a.flip, hi ? zc[1] : zc[0], hi ? sc[1] : sc[0], d);
+                            sts128_addr(aline + (uint32_t)((ch ^ (r & 7)) * 16), d);
+                        }
+                    } else {
+                        ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
+                        if (!ok) break;
+                        // 64 code bytes: chunks 4(q & 1) .. + 3 of the row in box q / 2
+                        const uint32_t box = prow + (uint32_t)((q >> 1) * (kPairBlock * 128));
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int cc = (c + q) & 3;              // channels 16·cc .. + 15
+                            const uint4 vv = lds128_addr(box + (uint32_t)(((4 * (q & 1) + cc) ^ (r & 7)) * 16));
+                            const bool hi = cc >= 2;
+                            uint32_t d[4];
+                            pair_dequant8<8>(vv.x, vv.y, a.flip, hi ? zc[1] : zc[0], hi ? sc[1] : sc[0], d);
+                            sts128_addr(aline + (uint32_t)(((2 * cc) ^ (r & 7)) * 16), d);
+                            pair_dequant8<8>(vv.z, vv.w, a.flip, hi ? zc[1] : zc[0], hi ? sc[1] : sc[0], d);
+                            sts128_addr(aline + (uint32_t)(((2 * cc + 1) ^ (r & 7)) * 16), d);
+                        }
                     }
                     release();
-                    unit_done();
                 }
             }
             // -------------------------------------------------------- epilogue

@@ -25,20 +25,24 @@
 // (64 channels contiguous per 128-byte swizzled line, lines along the rows), which the
 // tensor core reads as the transposed A operand; nothing is transposed in memory.
 //
-// Warps: 0 loads tokens (TMA, 128-byte swizzle), 18 loads codes (TMA), 1 issues the MMAs
-// and owns the tensor memory, 2..17 dequantize and run the epilogue.  Three rings of
+// Warps: 0 loads tokens (TMA, 128-byte swizzle), 2 loads codes (TMA), 1 issues the MMAs
+// and owns the tensor memory, 4..11 dequantize and run the epilogue (eight, so that a
+// thread has up to 168 registers; sixteen warps of 96 spilled and were slower).  Three rings of
 // shared memory, because the three have different sizes and lead times: token blocks,
 // code units (GATED with 4 bits: 128 input channels, so that a row is 64 bytes; loaded as
 // 32-byte rows the TMA engine's row rate, not bandwidth, paced the kernel) and dequantized
-// A tiles.  Each dequantizing thread holds the next block's codes in registers while it
-// works on the current one.  Scales and zero points go from global memory to registers
+// A tiles.  Scales and zero points go from global memory to registers
 // ahead of their block, so any number of groups per row and any alignment is read the
 // same way.
 //
-// The kernel is persistent, one CTA (or pair) per SM (or two): whole tiles are dealt in
-// turn, and what is left (or everything, when there are fewer tiles than CTAs) may be
-// split evenly along the reduction; then each CTA leaves binary32 parts of at most two
-// tiles, which pair_reduce_kernel adds in a fixed order.
+// The kernel is persistent, one CTA (or pair) per SM (or two).  Either whole tiles are
+// dealt in turn, or (when that would leave CTAs idle for longer than it costs) all tiles'
+// code units, in order, are divided evenly over the CTAs.  Then a tile may belong to
+// several CTAs: each owner but the first leaves its binary32 part in the workspace, with a
+// ready flag per warp, and the first owner adds the parts in order and finishes the tile.
+// A CTA leaves a part for its first tile only and waits only in its last one, so a part
+// has usually been there for a while, nothing waits in a circle, and the epilogues of the
+// CTAs are spread over time instead of all writing at once.
 #pragma once
 
 #include "activation.cuh"
@@ -165,9 +169,9 @@ constexpr uint32_t kIdescAMnMajor = 1u << 15;
 constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
 // ------------------------------------------------------------------ configuration
-constexpr int kPairDequantWarps = 16;
-constexpr int kPairCodeWarp = 2 + kPairDequantWarps;
-constexpr int kPairThreads = (kPairCodeWarp + 1) * 32;
+constexpr int kPairDequantWarps = 8;     // warps 4 .. 11, in two groups of four
+constexpr int kPairCodeWarp = 2;
+constexpr int kPairThreads = (4 + kPairDequantWarps) * 32;
 constexpr int kPairBlock = 64;          // reduction per block
 constexpr int kPairRows = 128;          // rows of one A tile per CTA
 constexpr int kPairABytes = 2 * kPairRows * kPairBlock * 2;   // both A tiles of a block: 32 KB
@@ -194,7 +198,7 @@ struct PairArgs {
     uint16_t* out;               // GATED: H [M, N]; DGRAD: dX [M, K]
     uint16_t* G;                 // GATED: kept outputs, or null
     uint16_t* U;
-    float* partials;             // split reduction: binary32 parts
+    float* partials;             // split: [slots][CTAs of a slot] binary32 parts
     int M, N, K;
     int gshift;                  // log2 g; 31 for per-channel (one group per row)
     int groups;                  // groups per row
@@ -206,55 +210,85 @@ struct PairArgs {
     int acc_cols;                // tensor-memory columns of one accumulator (power of two)
     int blocks;                  // reduction blocks of a tile
     int tiles_m;
-    int whole;                   // tiles [0, whole) are computed whole, dealt in turn
-    int tiles;                   // the others [whole, tiles) are split evenly ...
-    int sharers;                 // ... over this many CTAs (pairs), in code units; 0: none
+    int tiles;
+    int split;                   // 1: the tiles' code units are divided evenly over the CTAs
+    uint64_t* flags;             // [slots][CTAs of a slot][8] ready flags of the parts
 };
 
-// A CTA's (pair's) share of the work: whole tiles first, then its range of the split
-// tiles' units, as segments (tile, first unit, units).
+// Ready flag of a part: no sum, index or bf16 data is likely to hold it, so the workspace
+// needs no clearing before its first use; the first owner clears a flag that it consumed.
+constexpr uint64_t kPairFlagReady = 0x9E6C63D07F8A5C3Dull;
+
+// A CTA's (pair's) share of the work, as segments (tile, first unit, units).  The host
+// refuses problems of 2^31 units and more.
 template <int UB>
 struct PairWalk {
-    int slots, slot, upt;        // CTAs (pairs), this one, units per tile
     int tile, u0, units;
-    int64_t at, end;             // split range still to do
-    int part;                    // index of a split segment's part, -1 for a whole tile
-    __device__ __forceinline__ void init(const PairArgs& a, int slots_, int slot_) {
-        slots = slots_;
-        slot = slot_;
-        upt = (a.blocks + UB - 1) / UB;
-        tile = slot - slots;
-        at = end = 0;
-        if (a.sharers > 0 && slot < a.sharers) {
-            const int64_t total = (int64_t)(a.tiles - a.whole) * upt;
-            at = total * slot / a.sharers;
-            end = total * (slot + 1) / a.sharers;
-        }
-        part = -1;
+    int at, end;                 // split: this share's units still to do
+    __device__ __forceinline__ static int upt(const PairArgs& a) { return (a.blocks + UB - 1) / UB; }
+    // First unit of a slot's share.
+    __device__ __forceinline__ static int start(const PairArgs& a, int c, int slots) {
+        return (int)((int64_t)a.tiles * upt(a) * c / slots);
     }
-    __device__ __forceinline__ bool next(const PairArgs& a) {
-        if (part < 0) {
+    __device__ __forceinline__ void init(const PairArgs& a, int slot, int slots) {
+        tile = slot - slots;
+        at = a.split ? start(a, slot, slots) : 0;
+        end = a.split ? start(a, slot + 1, slots) : 0;
+    }
+    __device__ __forceinline__ bool next(const PairArgs& a, int slots) {
+        const int per = upt(a);
+        if (!a.split) {
             tile += slots;
-            if (tile < a.whole) {
-                u0 = 0;
-                units = upt;
-                return true;
-            }
+            u0 = 0;
+            units = per;
+            return tile < a.tiles;
         }
         if (at >= end) return false;
-        ++part;                              // 0, then 1
-        tile = a.whole + (int)(at / upt);
-        u0 = (int)(at % upt);
-        units = (int)(end - at < upt - u0 ? end - at : upt - u0);
+        tile = at / per;
+        u0 = at - tile * per;
+        units = min(end - at, per - u0);
         at += units;
         return true;
     }
     __device__ __forceinline__ int first_block() const { return u0 * UB; }
-    __device__ __forceinline__ int count(const PairArgs& a) const {
-        const int last = (u0 + units) * UB;
-        return (last < a.blocks ? last : a.blocks) - u0 * UB;
+    __device__ __forceinline__ int count(const PairArgs& a) const { return min((u0 + units) * UB, a.blocks) - u0 * UB; }
+    // Slots [slot + 1, followers_end) hold the rest of the tile that this share begins.
+    __device__ __forceinline__ int followers_end(const PairArgs& a, int slot, int slots) const {
+        const int per = upt(a);
+        int c = slot + 1;
+        if (u0 == 0 && units < per)
+            while (c < slots && start(a, c, slots) < (tile + 1) * per) ++c;
+        return c;
     }
 };
+
+__device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t* p) {
+    uint64_t v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_release_u64(uint64_t* p, uint64_t v) {
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+
+// Wait for another CTA's part (bounded: about one second).
+__device__ __forceinline__ bool pair_wait_flag(const uint64_t* flag) {
+    uint64_t t0 = 0;
+    for (uint32_t tries = 1;; ++tries) {
+        if (ld_acquire_u64(flag) == kPairFlagReady) return true;
+        __nanosleep(100);
+        if ((tries & 63u) == 0u) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) {
+                t0 = now;
+            } else if (now - t0 > kWaitTimeoutNs) {
+                report_error(kErrMbarTimeout);
+                return false;
+            }
+        }
+    }
+}
 
 // Zero point as the dequantization wants it, from the bf16 pair (z, z): the pair of
 // 128 + z (4-bit codes), or the binary32 2^23 + z (8-bit codes).
@@ -307,6 +341,13 @@ __device__ __forceinline__ uint4 lds128_addr(uint32_t addr) {
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(addr));
+    return v;
+}
+
+// An 8-byte read of scales or zeros through the read-only path.
+__device__ __forceinline__ uint2 ldg_u64x(const void* p) {
+    uint2 v;
+    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return v;
 }
 
@@ -384,15 +425,22 @@ __device__ __forceinline__ void pair_emit(const PairArgs& a, float v0[16], float
             strip_store(v1, stage, a.U, m, a.M, c, a.N, lane);
         }
         // (the choice of the activation outside the loop)
-        if (a.act == W4A16_ACT_SILU) {
+        switch (a.act) {
+            case W4A16_ACT_SILU:
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v0[i] = act_value(W4A16_ACT_SILU, v0[i]) * v1[i];
-        } else if (a.act == W4A16_ACT_GELU) {
-#pragma unroll 1
-            for (int i = 0; i < 16; ++i) v0[i] = act_value(W4A16_ACT_GELU, v0[i]) * v1[i];
-        } else {
+                for (int i = 0; i < 16; ++i) v0[i] = act_value(W4A16_ACT_SILU, v0[i]) * v1[i];
+                break;
+            case W4A16_ACT_GELU:
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v0[i] = act_value(a.act, v0[i]) * v1[i];
+                for (int i = 0; i < 16; ++i) v0[i] = act_value(W4A16_ACT_GELU, v0[i]) * v1[i];
+                break;
+            case W4A16_ACT_GELU_TANH:
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v0[i] = act_value(W4A16_ACT_GELU_TANH, v0[i]) * v1[i];
+                break;
+            default:
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v0[i] = act_value(W4A16_ACT_RELU, v0[i]) * v1[i];
         }
         strip_store(v0, stage, a.out, m, a.M, c, a.N, lane);
     }
@@ -409,11 +457,104 @@ __host__ __device__ inline int64_t pair_part_floats(int tokens) {
     return (int64_t)((tokens + 15) / 16) * 4 * 2 * 16 * 32;
 }
 
+// A tile (or a CTA's share of one) whose MMAs have been issued.
+struct PairTileDone {
+    int r0, m0;
+    bool publish;                // leave the sums as a part
+    int slot, followers_end;     // parts of slots [slot + 1, followers_end) belong to the tile
+    uint32_t accf, phase;        // barrier: accumulators complete
+    uint32_t accempty;           // barrier (of the even CTA): accumulators read
+    uint32_t tmem, stage;
+};
+
+// The epilogue of one warp: its strips of the accumulators, finished or left as a part.
+template <bool PAIR, bool DGRAD>
+__device__ __forceinline__ bool pair_epilogue(const PairArgs& a, const PairTileDone& t, int rank, int w) {
+    constexpr int kCtas = PAIR ? 2 : 1;
+    const int lane = threadIdx.x & 31;
+    const int mma_n = kCtas * a.bt;
+    bool ok = mbar_wait_cluster(t.accf, t.phase);
+    if (!ok) return false;
+    tc_fence_after();
+    const int quarter = w & 3;                         // the lanes this warp may read
+    const int strips = (min(mma_n, a.M - t.m0) + 15) / 16;
+    const uint32_t t_lane = t.tmem + ((uint32_t)(quarter * 32) << 16);
+    const int64_t part_floats = pair_part_floats(mma_n);
+    for (int c = t.slot + 1; c < t.followers_end && ok; ++c)
+        ok = pair_wait_flag(a.flags + ((int64_t)c * kCtas + rank) * kPairDequantWarps + w);
+    if (!__all_sync(0xffffffffu, ok ? 1 : 0)) return false;
+    // strips of this warp: the quarter's strips are dealt over its two warps
+#pragma unroll 1
+    for (int sidx = w >> 2; sidx < strips; sidx += kPairDequantWarps / 4) {
+        uint32_t v0[16], v1[16];
+        const uint32_t t0 = t_lane + 16 * sidx;
+        tmem_ld_16x256b_x2(t0, v0);
+        tmem_ld_16x256b_x2(t0 + (16u << 16), v0 + 8);
+        tmem_ld_16x256b_x2(t0 + a.acc_cols, v1);
+        tmem_ld_16x256b_x2(t0 + a.acc_cols + (16u << 16), v1 + 8);
+        tmem_wait_ld();
+        if (sidx + kPairDequantWarps / 4 >= strips) {
+            // the last of them is in registers: the next tile may have the accumulators
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (PAIR) mbar_arrive_cluster(t.accempty);
+                else mbar_arrive(t.accempty);
+            }
+        }
+        float f0[16], f1[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            f0[e] = __uint_as_float(v0[e]);
+            f1[e] = __uint_as_float(v1[e]);
+        }
+        // place of the strip in a CTA's part: 8 float4 per lane, lanes side by side
+        const int64_t in_part = (int64_t)(sidx * 4 + quarter) * (2 * 16 * 32);
+        if (t.publish) {
+            float4* part =
+                reinterpret_cast<float4*>(a.partials + ((int64_t)t.slot * kCtas + rank) * part_floats + in_part);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                part[e * 32 + lane] = make_float4(f0[4 * e], f0[4 * e + 1], f0[4 * e + 2], f0[4 * e + 3]);
+                part[(4 + e) * 32 + lane] = make_float4(f1[4 * e], f1[4 * e + 1], f1[4 * e + 2], f1[4 * e + 3]);
+            }
+            continue;
+        }
+        for (int c = t.slot + 1; c < t.followers_end; ++c) {
+            const float4* part =
+                reinterpret_cast<const float4*>(a.partials + ((int64_t)c * kCtas + rank) * part_floats + in_part);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 p = __ldcg(part + e * 32 + lane), q = __ldcg(part + (4 + e) * 32 + lane);
+                f0[4 * e] += p.x; f0[4 * e + 1] += p.y; f0[4 * e + 2] += p.z; f0[4 * e + 3] += p.w;
+                f1[4 * e] += q.x; f1[4 * e + 1] += q.y; f1[4 * e + 2] += q.z; f1[4 * e + 3] += q.w;
+            }
+        }
+        pair_emit<DGRAD>(a, f0, f1, t.stage, t.r0, rank, quarter, t.m0 + 16 * sidx, lane);
+    }
+    if ((w >> 2) >= strips && lane == 0) {             // no strip for this warp
+        if constexpr (PAIR) mbar_arrive_cluster(t.accempty);
+        else mbar_arrive(t.accempty);
+    }
+    if (t.publish) {
+        __threadfence();                               // every lane's part before the flag
+        __syncwarp();
+        if (lane == 0)
+            st_release_u64(a.flags + ((int64_t)t.slot * kCtas + rank) * kPairDequantWarps + w, kPairFlagReady);
+    } else if (t.followers_end > t.slot + 1) {
+        __syncwarp();
+        if (lane == 0)                                 // the parts were read: their flags are free again
+            for (int c = t.slot + 1; c < t.followers_end; ++c)
+                a.flags[((int64_t)c * kCtas + rank) * kPairDequantWarps + w] = 0ull;
+    }
+    return true;
+}
+
 template <bool PAIR, int BITS, bool DGRAD>
 __global__ void __launch_bounds__(kPairThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmX0, const __grid_constant__ CUtensorMap tmX1,
                      const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmP1,
-                     const PairArgs a) {
+                     const __grid_constant__ PairArgs a) {
     using Unit = PairUnit<BITS, DGRAD>;
     constexpr int UB = Unit::kBlocks, SP = Unit::kSlots, NA = kPairABufs;
     constexpr int kCtas = PAIR ? 2 : 1;
@@ -430,8 +571,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t xfull = bars, xempty = xfull + 8 * kPairMaxX;
     const uint32_t pfull = xempty + 8 * kPairMaxX, pempty = pfull + 8 * SP;
     const uint32_t afull = pempty + 8 * SP, aempty = afull + 8 * NA;
-    const uint32_t accf = aempty + 8 * NA;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + (accf + 8 - as));
+    const uint32_t accf = aempty + 8 * NA, accempty = accf + 8;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + (accempty + 8 - as));
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -454,6 +595,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(aempty + 8 * s, 1);
         }
         mbar_init(accf, 1);
+        mbar_init(accempty, kCtas * kPairDequantWarps);
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
@@ -472,7 +614,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     tc_fence_after();
     const uint32_t tmem_d = *tmem_holder;
     PairWalk<UB> walk;
-    walk.init(a, slots, slot);
+    walk.init(a, slot, slots);
 
     if (warp == 0) {
         // ------------------------------------------------------------ token loads
@@ -480,7 +622,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int s = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
-            while (ok && walk.next(a)) {
+            while (ok && walk.next(a, slots)) {
                 const int b0 = walk.first_block(), nb = walk.count(a);
                 const int m0 = walk.tile % a.tiles_m * mma_n + rank * a.bt;
                 for (int i = 0; i < nb; ++i) {
@@ -509,7 +651,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int s = 0, issued = 0;
             uint32_t ph = 0;
             bool ok = true;
-            while (ok && walk.next(a)) {
+            while (ok && walk.next(a, slots)) {
                 const int r0 = pair_row0<DGRAD>(a, walk.tile, kCtas);
                 for (int u = 0; u < walk.units; ++u) {
                     ok = mbar_wait(pempty + 8 * s, ph ^ 1u);
@@ -544,12 +686,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // ------------------------------------------------------------ MMA issue (even CTA)
         if (lane == 0 && rank == 0) {
             const uint32_t idesc = idesc_bf16_f32(kCtas * kPairRows, mma_n) | (DGRAD ? kIdescAMnMajor : 0u);
-            int s = 0, ab = 0;
+            int s = 0, ab = 0, seg = 0;
             uint32_t pa = 0;
             bool ok = true;
-            while (ok && walk.next(a)) {
+            while (ok && walk.next(a, slots)) {
                 const int nb = walk.count(a);
-                for (int i = 0; i < nb; ++i) {
+                // both CTAs' warps have read the previous tile's accumulators
+                if (seg > 0) ok = mbar_wait_cluster(accempty, (uint32_t)(seg - 1) & 1u);
+                ++seg;
+                for (int i = 0; i < nb && ok; ++i) {
                     // (a dequantizing warp of each CTA arrives after the tokens landed there too)
                     ok = mbar_wait_cluster(afull + 8 * ab, pa);
                     if (!ok) break;
@@ -576,19 +721,43 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp >= 4) {
         // ------------------------------------------------------------ dequantize, epilogue
-        // Two groups of eight warps take the blocks in turn, so that one group's waits, fences
+        // Two groups of four warps take the blocks in turn, so that one group's waits, fences
         // and loads hide behind the other's arithmetic and each warp pays its per-block
-        // overhead for eight chunks of codes.
-        const int w = warp - 2, grp = w >> 3, wg = w & 7;
+        // overhead for sixteen chunks of codes.
+        const int w = warp - 4, grp = w >> 2, wg = w & 3;
         const bool sym = a.flip != 0u;
         const uint32_t afull_r = PAIR ? mapa_u32(afull, 0) : afull;
         int cnt = 0, ucnt = 0, seg = 0;              // blocks and units of the segments before
         bool ok = true;
-        while (ok && walk.next(a)) {
-            const int r0 = pair_row0<DGRAD>(a, walk.tile, kCtas);
-            const int b0 = walk.first_block(), nb = walk.count(a);
+        // A finished tile's epilogue runs after the next segment's first NA blocks were
+        // dequantized, while its own last MMAs complete: the pipeline is full again when the
+        // accumulators are free.
+        bool pending = false, e_publish = false;
+        int e_r0 = 0, e_m0 = 0, e_f1 = 0;
+
+        auto epilogue = [&]() {
+            PairTileDone t;
+            t.r0 = e_r0;
+            t.m0 = e_m0;
+            t.publish = e_publish;
+            t.slot = slot;
+            t.followers_end = e_f1;
+            t.accf = accf;
+            t.phase = (uint32_t)seg & 1u;
+            t.accempty = PAIR ? mapa_u32(accempty, 0) : accempty;
+            t.tmem = tmem_d;
+            t.stage = st + w * 1024;
+            ok = pair_epilogue<PAIR, DGRAD>(a, t, rank, w);
+            ++seg;
+        };
+
+        while (ok) {
+            const bool more = walk.next(a, slots);
+            if (!more && !pending) break;
+            const int nb = more ? walk.count(a) : 0, b0 = more ? walk.first_block() : 0;
+            const int r0 = more ? pair_row0<DGRAD>(a, walk.tile, kCtas) : 0;
             // this group's first block in each ring: slot and phase
             int ab = (cnt + grp) % NA, xslot = (cnt + grp) % SX;
             uint32_t aph = (uint32_t)((cnt + grp) / NA) & 1u, xph = (uint32_t)((cnt + grp) / SX) & 1u;
@@ -596,7 +765,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int pslot = ufirst % SP;
             uint32_t pph = (uint32_t)(ufirst / SP) & 1u;
             cnt += nb;
-            ucnt += walk.units;
+            if (more) ucnt += walk.units;
             // The A tiles of a block are written: visible to the tensor core, then counted; the
             // codes were used, so their slot is given back.  (Given back right behind the
             // loads, a slot was seen refilled before a load of it had been performed.)
@@ -617,85 +786,107 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 pslot += UB == 2 ? 1 : 2;
                 if (pslot >= SP) { pslot -= SP; pph ^= 1u; }
             };
+            int i = grp;
             if constexpr (!DGRAD) {
-                // thread = row r of both matrices, 32-wide half h of the block
-                const int r = (wg & 3) * 32 + lane, h = wg >> 2;
-                const int n = r0 + rank * kPairRows + r;
-                const bool row_ok = n < a.N;
-                const bool vec = (a.groups & 7) == 0;         // rows of scales are 16-byte aligned
-                const int64_t srow = (int64_t)(row_ok ? n : 0) * a.groups;
-                const uint32_t sts0 = (uint32_t)(r * 128 + (((4 * h) ^ (r & 7)) * 16));   // chunk c: ^ 16·c
+                // thread = row r of both matrices
+                const int r = wg * 32 + lane;
+                // (a row behind the last reads the last row's scales: its results are dropped)
+                const int n = min(r0 + rank * kPairRows + r, a.N - 1);
+                const bool vec = (a.groups & 3) == 0;         // rows of scales are 8-byte aligned
+                const int64_t srow = (int64_t)n * a.groups;
+                const uint32_t sts0 = (uint32_t)(r * 128 + ((r & 7) * 16));               // chunk c: ^ 16·c
                 const uint32_t lds0 = ps + (uint32_t)(r * 64) +
-                                      (uint32_t)(((BITS == 4 ? 2 * grp + h : 2 * h) ^ ((r >> 1) & 3)) * 16);
-                uint32_t ss[2], zz[2];                        // the current group's pairs
+                                      (uint32_t)(((BITS == 4 ? 2 * grp : 0) ^ ((r >> 1) & 3)) * 16);
+                auto group_of = [&](int blk, int h) {
+                    return min(((b0 + blk) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
+                };
+                // Scales and zeros: four groups at hand and the next four on their way, or (rows
+                // of another alignment) the two halves' groups of this block and of the next
+                // one of this warp.  [scale, zero][matrix]
+                uint2 cur[2][2], nxt[2][2];
+                uint32_t sc[2][2], zc[2][2];                  // pairs of [matrix][half of the block]
                 int have = -1;
-                if (!vec) {
-                    // the pair of the group ahead, loaded one change early
-                    const int g0 = min(((b0 + grp) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
+                auto fetch = [&](uint2 (&to)[2][2], int blk) {
+                    const int ga = group_of(blk, 0), gb = group_of(blk, 1);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        ss[j] = row_ok ? ldg_u16(a.scales[j] + srow + g0) : 0u;
-                        zz[j] = row_ok && !sym ? ldg_u16(a.zeros[j] + srow + g0) : 0u;
-                    }
-                }
-                uint4 s8[2], z8[2];                           // eight groups of the row
-                uint32_t sc[2] = {0u, 0u}, zc[2] = {0u, 0u};
-                for (int i = grp; i < nb && ok; i += 2) {
-                    const int g = min(((b0 + i) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
-                    if (g != have) {
-                        if (vec) {
-                            if (have < 0 || (g >> 3) != (have >> 3)) {
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            if (t == 1 && sym) continue;
+                            const uint16_t* p = (t == 0 ? a.scales[j] : a.zeros[j]) + srow;
+                            if (vec) {
+                                to[t][j] = ldg_u64x(p + (ga & ~3));
+                            } else {
+                                to[t][j].x = ldg_u16(p + ga);
+                                to[t][j].y = ldg_u16(p + gb);
+                            }
+                        }
+                };
+                // first block of this warp whose scales lie behind those at hand
+                auto beyond = [&](int blk) {
+                    if (!vec) return blk + 2;
+                    const int k = ((((group_of(blk, 0) >> 2) + 1) * 4) << a.gshift) / kPairBlock - b0;
+                    return max(blk + 2, k + ((k ^ grp) & 1));
+                };
+#pragma unroll
+                for (int j = 0; j < 2; ++j) cur[0][j] = cur[1][j] = nxt[0][j] = nxt[1][j] = make_uint2(0u, 0u);
+                if (more) fetch(nxt, grp);
+                for (int phase = pending ? 0 : 1; phase < 2; ++phase) {
+                    const int hi = phase == 0 ? min(nb, NA) : nb;
+                    for (; i < hi && ok; i += 2) {
+                        const int ga = group_of(i, 0), gb = group_of(i, 1);
+                        if (ga != have || gb != ga) {
+                            if (!vec || have < 0 || (ga >> 2) != (have >> 2)) {
+#pragma unroll
+                                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                                    for (int j = 0; j < 2; ++j) cur[t][j] = nxt[t][j];
+                                fetch(nxt, beyond(i));
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int g = h ? gb : ga;
+                                const uint32_t sel = vec && (g & 1) ? 0x3232u : 0x1010u;
+                                const bool up = vec ? (g & 2) != 0 : h == 1;
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
-                                    s8[j] = row_ok ? ldg_cached(a.scales[j] + srow + (g & ~7)) : make_uint4(0, 0, 0, 0);
-                                    z8[j] = row_ok && !sym ? ldg_cached(a.zeros[j] + srow + (g & ~7)) : make_uint4(0, 0, 0, 0);
+                                    sc[j][h] = __byte_perm(up ? cur[0][j].y : cur[0][j].x, 0u, sel);
+                                    zc[j][h] = pair_zero<BITS>(__byte_perm(up ? cur[1][j].y : cur[1][j].x, 0u, sel), sym, a.zsym);
                                 }
                             }
-                            const bool up = (g & 4) != 0, odd = (g & 2) != 0;
-                            const uint32_t sel = (g & 1) ? 0x3232u : 0x1010u;
+                            have = ga;
+                        }
+                        ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
+                        uint4 v[2][BITS / 2];
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const uint32_t s0 = up ? s8[j].z : s8[j].x, s1 = up ? s8[j].w : s8[j].y;
-                                const uint32_t z0 = up ? z8[j].z : z8[j].x, z1 = up ? z8[j].w : z8[j].y;
-                                sc[j] = __byte_perm(odd ? s1 : s0, 0u, sel);
-                                zc[j] = pair_zero<BITS>(__byte_perm(odd ? z1 : z0, 0u, sel), sym, a.zsym);
-                            }
-                        } else {
-                            const int gn = min(((b0 + i + 2) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
-                            const int ahead = gn != g ? gn : min(g + 1, a.groups - 1);
+                        for (int j = 0; j < 2; ++j)
 #pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                sc[j] = dup16(ss[j]);
-                                zc[j] = pair_zero<BITS>(dup16(zz[j]), sym, a.zsym);
-                                ss[j] = row_ok ? ldg_u16(a.scales[j] + srow + ahead) : 0u;
-                                zz[j] = row_ok && !sym ? ldg_u16(a.zeros[j] + srow + ahead) : 0u;
+                            for (int c = 0; c < BITS / 2; ++c)
+                                v[j][c] = lds128_addr((lds0 + (uint32_t)(pslot * Unit::kBytes + j * (Unit::kBytes / 2))) ^
+                                                      (uint32_t)(16 * c));
+                        ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
+                        if (!ok) break;
+                        const uint32_t arow = as + (uint32_t)(ab * kPairABytes) + sts0;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t d[4];
+                                if constexpr (BITS == 4) {
+                                    const uint4 q = v[j][c >> 2];
+                                    const uint32_t wd = (c & 3) == 0 ? q.x : ((c & 3) == 1 ? q.y : ((c & 3) == 2 ? q.z : q.w));
+                                    pair_dequant8<4>(wd, 0u, a.flip, zc[j][c >> 2], sc[j][c >> 2], d);
+                                } else {
+                                    const uint4 q = v[j][c >> 1];
+                                    pair_dequant8<8>((c & 1) ? q.z : q.x, (c & 1) ? q.w : q.y, a.flip, zc[j][c >> 2],
+                                                     sc[j][c >> 2], d);
+                                }
+                                sts128_addr((arow ^ (uint32_t)(16 * c)) + (uint32_t)(j * (kPairABytes / 2)), d);
                             }
                         }
-                        have = g;
+                        release();
                     }
-                    ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
-                    uint4 v[2], v8[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t at = lds0 + (uint32_t)(pslot * Unit::kBytes + j * (Unit::kBytes / 2));
-                        v[j] = lds128_addr(at);
-                        v8[j] = BITS == 8 ? lds128_addr(at ^ 16u) : make_uint4(0, 0, 0, 0);
-                    }
-                    ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
-                    if (!ok) break;
-                    const uint32_t arow = as + (uint32_t)(ab * kPairABytes) + sts0;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t wv[8] = {v[j].x, v[j].y, v[j].z, v[j].w, v8[j].x, v8[j].y, v8[j].z, v8[j].w};
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t d[4];
-                            if constexpr (BITS == 4) pair_dequant8<4>(wv[c], 0u, a.flip, zc[j], sc[j], d);
-                            else pair_dequant8<8>(wv[2 * c], wv[2 * c + 1], a.flip, zc[j], sc[j], d);
-                            sts128_addr((arow ^ (uint32_t)(16 * c)) + (uint32_t)(j * (kPairABytes / 2)), d);
-                        }
-                    }
-                    release();
+                    if (phase == 0 && ok) epilogue();
                 }
                 if (UB == 2 && ok && grp == 1 && (nb & 1)) {
                     // the segment's last unit has no block for this group
@@ -703,132 +894,101 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if (lane == 0) mbar_arrive(pempty + 8 * pslot);
                 }
             } else {
-                // thread = weight row r of the block, 64-channel block q: the four threads of a row
-                // are neighbours, so that a warp's scale loads touch eight rows.  Each starts
-                // at another chunk (2q), which keeps its shared-memory stores off the banks
-                // of the other three.
-                const int r = wg * 8 + (lane >> 2), q = lane & 3;
-                const int c0 = r0 + rank * 2 * kPairRows + 64 * q;       // first input channel
-                const bool chan_ok = c0 < a.K;
-                const int g0 = min(c0 >> a.gshift, a.groups - 1), g1 = min((c0 + 32) >> a.gshift, a.groups - 1);
-                auto fetch = [&](int i, uint32_t* sb, uint32_t* zb) {
-                    int b = b0 + i;
+                // thread = weight row r of the block, 128 channels (one A tile) q: a warp's scale
+                // loads touch sixteen rows.  The two threads of a row take their chunks in
+                // orders that differ by 4, which keeps their shared-memory stores on
+                // different banks.
+                const int r = wg * 16 + (lane >> 1), q = lane & 1;
+                const int c0 = r0 + rank * 2 * kPairRows + 128 * q;      // first input channel
+                // (a row or channel behind the last reads the last one's pair: the tokens' values
+                // there are zeros, or the results are dropped)
+                const int pieces = a.gshift >= 7 ? 1 : (a.gshift == 6 ? 2 : 4);   // groups in 128 channels
+                const int g0 = c0 >> a.gshift, glast = a.groups - 1;
+                auto fetch = [&](int blk, uint32_t (&sb)[4], uint32_t (&zb)[4]) {
+                    int b = b0 + min(blk, nb - 1);
                     const bool second = b >= per_product;
                     if (second) b -= per_product;
-                    const int n = b * kPairBlock + r;
-                    sb[0] = sb[1] = zb[0] = zb[1] = 0u;
-                    if (i < nb && n < a.N && chan_ok) {
-                        const uint16_t* sp = (second ? a.scales[1] : a.scales[0]) + (int64_t)n * a.groups;
-                        const uint16_t* zp = (second ? a.zeros[1] : a.zeros[0]) + (int64_t)n * a.groups;
-                        sb[0] = ldg_u16(sp + g0);
-                        if (!sym) zb[0] = ldg_u16(zp + g0);
-                        if (g1 != g0) {
-                            sb[1] = ldg_u16(sp + g1);
-                            if (!sym) zb[1] = ldg_u16(zp + g1);
+                    const int64_t at = (int64_t)min(b * kPairBlock + r, a.N - 1) * a.groups;
+                    const uint16_t* sp = (second ? a.scales[1] : a.scales[0]) + at;
+                    const uint16_t* zp = (second ? a.zeros[1] : a.zeros[0]) + at;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        if (t < pieces) {
+                            sb[t] = ldg_u16(sp + min(g0 + t, glast));
+                            if (!sym) zb[t] = ldg_u16(zp + min(g0 + t, glast));
                         }
-                    }
                 };
                 // pairs of this group's next two blocks
-                uint32_t sn[2][2], zn[2][2];
-                fetch(grp, sn[0], zn[0]);
-                fetch(grp + 2, sn[1], zn[1]);
-                const uint32_t row = ps + (uint32_t)(r * 128);
-                const uint32_t line = as + (uint32_t)(q * 8192 + r * 128);
-                for (int i = grp; i < nb && ok; i += 2) {
-                    uint32_t sc[2], zc[2];
-                    sc[0] = dup16(sn[0][0]);
-                    zc[0] = pair_zero<BITS>(dup16(zn[0][0]), sym, a.zsym);
-                    sc[1] = g1 != g0 ? dup16(sn[0][1]) : sc[0];
-                    zc[1] = g1 != g0 ? pair_zero<BITS>(dup16(zn[0][1]), sym, a.zsym) : zc[0];
+                uint32_t sa[4], za[4], sn[4], zn[4];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        sn[0][t] = sn[1][t];
-                        zn[0][t] = zn[1][t];
-                    }
-                    fetch(i + 4, sn[1], zn[1]);
-                    ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
-                    const uint32_t prow = row + (uint32_t)(pslot * Unit::kBytes);
-                    const uint32_t aline = line + (uint32_t)(ab * kPairABytes);
-                    if constexpr (BITS == 4) {
-                        // 32 code bytes: logical chunks 2q, 2q + 1 of the row's eight (128-byte swizzle)
-                        const uint32_t at = prow + (uint32_t)(((2 * q) ^ (r & 7)) * 16);
-                        const uint4 va = lds128_addr(at), vb = lds128_addr(at ^ 16u);
-                        uint32_t u[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w}, v[8];
-                        // u rotated by 2q words: step c handles chunk (c + 2q) mod 8
+                for (int t = 0; t < 4; ++t) sa[t] = za[t] = sn[t] = zn[t] = 0u;
+                if (more) {
+                    fetch(grp, sa, za);
+                    fetch(grp + 2, sn, zn);
+                }
+                const uint32_t row = ps + (uint32_t)(r * 128 + (BITS == 8 ? q * (kPairBlock * 128) : 0));
+                const uint32_t line = as + (uint32_t)(q * (kPairABytes / 2) + r * 128 + (((4 * q) ^ (r & 7)) * 16));
+                for (int phase = pending ? 0 : 1; phase < 2; ++phase) {
+                    const int hi = phase == 0 ? min(nb, NA) : nb;
+                    for (; i < hi && ok; i += 2) {
+                        uint32_t sc[4], zc[4];                   // pairs of the four 32-channel pieces
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) v[c] = (q & 2) ? u[(c + 4) & 7] : u[c];
+                        for (int t = 0; t < 4; ++t) {
+                            const uint32_t sv = pieces == 4 ? sa[t] : (pieces == 2 ? sa[t >> 1] : sa[0]);
+                            const uint32_t zv = pieces == 4 ? za[t] : (pieces == 2 ? za[t >> 1] : za[0]);
+                            sc[t] = dup16(sv);
+                            zc[t] = pair_zero<BITS>(dup16(zv), sym, a.zsym);
+                        }
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) u[c] = (q & 1) ? v[(c + 2) & 7] : v[c];
+                        for (int t = 0; t < 4; ++t) {
+                            sa[t] = sn[t];
+                            za[t] = zn[t];
+                        }
+                        fetch(i + 4, sn, zn);
+                        ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
+                        const uint32_t prow = row + (uint32_t)(pslot * Unit::kBytes);
+                        uint4 v[BITS];                           // the thread's codes
+#pragma unroll
+                        for (int c = 0; c < BITS; ++c)
+                            v[c] = lds128_addr(prow + (uint32_t)((((BITS == 4 ? 4 * q : 0) + c) ^ (r & 7)) * 16));
                         ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
                         if (!ok) break;
+                        const uint32_t aline = line + (uint32_t)(ab * kPairABytes);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const int ch = (c + 2 * q) & 7;
-                            const bool hi = ch >= 4;
-                            uint32_t d[4];
-                            pair_dequant8<4>(u[c], 0u, a.flip, hi ? zc[1] : zc[0], hi ? sc[1] : sc[0], d);
-                            sts128_addr(aline + (uint32_t)((ch ^ (r & 7)) * 16), d);
-                        }
-                    } else {
-                        ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
-                        if (!ok) break;
-                        // 64 code bytes: chunks 4(q & 1) .. + 3 of the row in box q / 2
-                        const uint32_t box = prow + (uint32_t)((q >> 1) * (kPairBlock * 128));
+                        for (int b = 0; b < 2; ++b) {            // blocks of 64 channels
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            const int cc = (c + q) & 3;              // channels 16·cc .. + 15
-                            const uint4 vv = lds128_addr(box + (uint32_t)(((4 * (q & 1) + cc) ^ (r & 7)) * 16));
-                            const bool hi = cc >= 2;
-                            uint32_t d[4];
-                            pair_dequant8<8>(vv.x, vv.y, a.flip, hi ? zc[1] : zc[0], hi ? sc[1] : sc[0], d);
-                            sts128_addr(aline + (uint32_t)(((2 * cc) ^ (r & 7)) * 16), d);
-                            pair_dequant8<8>(vv.z, vv.w, a.flip, hi ? zc[1] : zc[0], hi ? sc[1] : sc[0], d);
-                            sts128_addr(aline + (uint32_t)(((2 * cc + 1) ^ (r & 7)) * 16), d);
+                            for (int c = 0; c < 8; ++c) {
+                                // step c: chunk c of thread 0, chunk c ^ 4 of thread 1
+                                const uint32_t ss = q ? sc[2 * b + 1 - (c >> 2)] : sc[2 * b + (c >> 2)];
+                                const uint32_t zz = q ? zc[2 * b + 1 - (c >> 2)] : zc[2 * b + (c >> 2)];
+                                uint32_t d[4];
+                                if constexpr (BITS == 4) {
+                                    const uint4 lo = v[2 * b + (c >> 2)], hi4 = v[2 * b + 1 - (c >> 2)];
+                                    const uint32_t wl = (c & 3) == 0 ? lo.x : ((c & 3) == 1 ? lo.y : ((c & 3) == 2 ? lo.z : lo.w));
+                                    const uint32_t wh = (c & 3) == 0 ? hi4.x : ((c & 3) == 1 ? hi4.y : ((c & 3) == 2 ? hi4.z : hi4.w));
+                                    pair_dequant8<4>(q ? wh : wl, 0u, a.flip, zz, ss, d);
+                                } else {
+                                    const uint4 x0 = v[4 * b + (c >> 1)], x1 = v[4 * b + ((c >> 1) ^ 2)];
+                                    const uint32_t w0 = (c & 1) ? (q ? x1.z : x0.z) : (q ? x1.x : x0.x);
+                                    const uint32_t w1 = (c & 1) ? (q ? x1.w : x0.w) : (q ? x1.y : x0.y);
+                                    pair_dequant8<8>(w0, w1, a.flip, zz, ss, d);
+                                }
+                                sts128_addr((aline ^ (uint32_t)(16 * c)) + (uint32_t)(b * 8192), d);
+                            }
                         }
+                        release();
                     }
-                    release();
+                    if (phase == 0 && ok) epilogue();
                 }
             }
-            // -------------------------------------------------------- epilogue
-            if (!ok || !mbar_wait_cluster(accf, (uint32_t)seg & 1u)) break;
-            ++seg;
-            tc_fence_after();
-            const int quarter = warp & 3;                      // the lanes this warp may read
-            const int m0 = walk.tile % a.tiles_m * mma_n;
-            const int strips = (min(mma_n, a.M - m0) + 15) / 16;
-            const uint32_t t_lane = tmem_d + ((uint32_t)(quarter * 32) << 16);
-            // which of the quarter's four warps this one is
-            for (int sidx = w >> 2; sidx < strips; sidx += kPairDequantWarps / 4) {
-                uint32_t v0[16], v1[16];
-                const uint32_t t0 = t_lane + 16 * sidx;
-                tmem_ld_16x256b_x2(t0, v0);
-                tmem_ld_16x256b_x2(t0 + (16u << 16), v0 + 8);
-                tmem_ld_16x256b_x2(t0 + a.acc_cols, v1);
-                tmem_ld_16x256b_x2(t0 + a.acc_cols + (16u << 16), v1 + 8);
-                tmem_wait_ld();
-                if (walk.part < 0) {
-                    float f0[16], f1[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        f0[e] = __uint_as_float(v0[e]);
-                        f1[e] = __uint_as_float(v1[e]);
-                    }
-                    pair_emit<DGRAD>(a, f0, f1, st + w * 1024, r0, rank, quarter, m0 + 16 * sidx, lane);
-                } else {
-                    float4* part = reinterpret_cast<float4*>(
-                        a.partials + ((int64_t)(slot * 2 + walk.part) * kCtas + rank) * pair_part_floats(mma_n) +
-                        (int64_t)(sidx * 4 + quarter) * (2 * 16 * 32));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        part[e * 32 + lane] = make_float4(__uint_as_float(v0[4 * e]), __uint_as_float(v0[4 * e + 1]),
-                                                          __uint_as_float(v0[4 * e + 2]), __uint_as_float(v0[4 * e + 3]));
-                        part[(4 + e) * 32 + lane] =
-                            make_float4(__uint_as_float(v1[4 * e]), __uint_as_float(v1[4 * e + 1]),
-                                        __uint_as_float(v1[4 * e + 2]), __uint_as_float(v1[4 * e + 3]));
-                    }
-                }
+            // this segment's epilogue waits for the next segment's first blocks
+            pending = more;
+            if (more) {
+                e_r0 = r0;
+                e_m0 = walk.tile % a.tiles_m * mma_n;
+                e_publish = walk.u0 != 0;
+                e_f1 = walk.followers_end(a, slot, slots);
             }
-            tc_fence_before();      // the reads above precede this warp's next arrival, hence the next MMA
         }
         __syncwarp();
     }
@@ -840,44 +1000,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tc_fence_after();
         tmem_dealloc_g<PAIR>(tmem_d, 2 * a.acc_cols);
     }
-}
-
-// Adds the parts of the split tiles in the order of the reduction and runs the epilogue:
-// one warp per strip of a CTA's rows, in the layout the parts were left in.
-constexpr int kPairReduceThreads = 128;
-template <bool DGRAD>
-__global__ void __launch_bounds__(kPairReduceThreads) pair_reduce_kernel(const PairArgs a, int ctas, int upt) {
-    __shared__ __align__(16) uint8_t stage[kPairReduceThreads / 32 * 1024];
-    grid_dependency_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int mma_n = ctas * a.bt, strips = (mma_n + 15) / 16;
-    const int64_t item = (int64_t)blockIdx.x * (kPairReduceThreads / 32) + warp;
-    const int quarter = (int)(item % 4), sidx = (int)(item / 4 % strips);
-    const int64_t rest = item / 4 / strips;
-    const int rank = (int)(rest % ctas), split = (int)(rest / ctas);
-    const int tile = a.whole + split;
-    if (tile >= a.tiles) return;
-    const int m = tile % a.tiles_m * mma_n + 16 * sidx;
-    if (m >= a.M) return;
-    const int64_t total = (int64_t)(a.tiles - a.whole) * upt, u0 = (int64_t)split * upt, u1 = u0 + upt;
-    // sharer c holds units [total·c/S, total·(c + 1)/S)
-    const int first = (int)(((u0 + 1) * a.sharers - 1) / total), last = (int)((u1 * a.sharers - 1) / total);
-    float v0[16], v1[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) v0[e] = v1[e] = 0.0f;
-    for (int c = first; c <= last; ++c) {
-        const int seg = total * c / a.sharers >= u0 ? 0 : 1;       // the tile is the sharer's first or second
-        const float4* part = reinterpret_cast<const float4*>(
-            a.partials + ((int64_t)(c * 2 + seg) * ctas + rank) * pair_part_floats(mma_n) +
-            (int64_t)(sidx * 4 + quarter) * (2 * 16 * 32));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float4 p = __ldcg(part + e * 32 + lane), q = __ldcg(part + (4 + e) * 32 + lane);
-            v0[4 * e] += p.x; v0[4 * e + 1] += p.y; v0[4 * e + 2] += p.z; v0[4 * e + 3] += p.w;
-            v1[4 * e] += q.x; v1[4 * e + 1] += q.y; v1[4 * e + 2] += q.z; v1[4 * e + 3] += q.w;
-        }
-    }
-    pair_emit<DGRAD>(a, v0, v1, smem_u32(stage) + warp * 1024, pair_row0<DGRAD>(a, tile, ctas), rank, quarter, m, lane);
 }
 
 }  // namespace w4a16

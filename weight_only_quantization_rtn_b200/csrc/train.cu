@@ -68,10 +68,9 @@ struct PairPlan {
     int upt;           // code units per tile
     int tiles_m;
     int64_t tiles;
-    int64_t whole;     // tiles computed whole
-    int sharers;       // CTAs (pairs) that share the others
+    int split;         // 1: the tiles' units are divided evenly over the CTAs (pairs)
     int grid;          // CTAs (pairs) launched
-    int64_t bytes;     // workspace of the parts
+    int64_t flag_bytes, bytes;   // workspace: ready flags, then parts
 };
 
 // `rows` output rows (features or input channels) in tiles of `rows_per_cta` per CTA.
@@ -79,42 +78,37 @@ struct PairPlan {
 // Token tile: the batch in equal tiles of at most 128 tokens for one CTA (one tile) and
 // 256 for a pair, in steps of 16.
 //
-// Split: whole waves of tiles are dealt as they are.  The rest leaves CTAs without work;
-// splitting it over all of them along the reduction saves the idle share of a tile's time
-// and costs writing and reading binary32 parts and a second kernel.  Both sides are
-// estimated and the smaller taken: a block takes about 0.55 us per 256 tokens, at least
-// 0.25 us (dequantization); parts move at about 3 TB/s, the second kernel takes 3 us.
+// Split: whole tiles in waves leave CTAs idle in the last one.  Dividing all units evenly
+// ends that, and costs each CTA writing one part and reading one.  Both times are
+// estimated and the smaller taken: a block takes about 0.6 us per 256 tokens and at least
+// 0.22 us (dequantization), a CTA moves a part at about 80 GB/s, and 2 us go to the flags.
 PairPlan pair_plan(int64_t M, int64_t rows, int rows_per_cta, int64_t blocks, int unit_blocks, int sm_count) {
     PairPlan p{};
     p.ctas = M > 128 ? 2 : 1;
     const int64_t most = p.ctas == 2 ? 256 : 128;
     const int64_t tiles_m = (M + most - 1) / most;
-    const int64_t tokens = ((M + tiles_m - 1) / tiles_m + 15) / 16 * 16;
+    const int64_t tokens = tiles_m > 0 ? ((M + tiles_m - 1) / tiles_m + 15) / 16 * 16 : 16;
     p.bt = (int)(tokens / p.ctas);
     p.tiles_m = (int)tiles_m;
     p.tiles = tiles_m * ((rows + rows_per_cta * p.ctas - 1) / (rows_per_cta * p.ctas));
     p.blocks = (int)blocks;
-    p.upt = (int)((blocks + unit_blocks - 1) / unit_blocks);
+    const int64_t units = (blocks + unit_blocks - 1) / unit_blocks;
     const int64_t slots = sm_count / p.ctas;
-    p.whole = p.tiles / slots * slots;
-    const int64_t rest = p.tiles - p.whole;
-    if (rest > 0) {
-        const int64_t part = pair_part_floats((int)tokens) * 4 * p.ctas;
-        // at least two units of work for each sharer
-        int64_t sharers = rest * p.upt / 2;
-        if (sharers > slots) sharers = slots;
-        const double block_us = tokens * 0.55 / 256 > 0.25 ? tokens * 0.55 / 256 : 0.25;
-        const double saved = blocks * block_us * (1.0 - (double)rest / (double)sharers);
-        const double paid = 3.0 + 2.0 * (double)((rest + sharers) * part) / 3e6;
-        if (sharers > rest && saved > paid) {
-            p.sharers = (int)sharers;
-            p.bytes = sharers * 2 * part;
-        } else {
-            p.whole = p.tiles;
+    p.grid = (int)(p.tiles < slots ? p.tiles : slots);
+    int64_t sharers = p.tiles * units / 2;             // two units at least for each
+    if (sharers > slots) sharers = slots;
+    if (sharers > p.grid || p.tiles % slots != 0) {
+        const int64_t part = pair_part_floats((int)tokens) * 4;
+        const double block_us = tokens * 0.6 / 256 > 0.22 ? tokens * 0.6 / 256 : 0.22;
+        const double whole = (double)((p.tiles + slots - 1) / slots) * blocks * block_us;
+        const double split = (double)p.tiles * blocks * block_us / (double)sharers + 2.0 + 2.0 * part / 80e3;
+        if (sharers >= p.grid && split < whole) {
+            p.split = 1;
+            p.grid = (int)sharers;
+            p.flag_bytes = round256(sharers * p.ctas * kPairDequantWarps * 8);
+            p.bytes = p.flag_bytes + sharers * p.ctas * part;
         }
     }
-    p.grid = (int)(p.whole < slots ? p.whole : slots);
-    if (p.sharers > p.grid) p.grid = p.sharers;
     return p;
 }
 
@@ -138,7 +132,7 @@ w4a16_status launch_chained(void (*kern)(A...), dim3 grid, int threads, cudaStre
 
 template <bool PAIR, int BITS, bool DGRAD>
 w4a16_status launch_pair_t(const PairPlan& p, const CUtensorMap* tmX, const CUtensorMap* tmP, PairArgs args,
-                           cudaStream_t stream) {
+                           void* workspace, cudaStream_t stream) {
     auto kern = gemm_pair_kernel<PAIR, BITS, DGRAD>;
     static bool done[kMaxDevices] = {};
     w4a16_status st = set_smem(kern, kPairSmemBytes, done);
@@ -148,9 +142,12 @@ w4a16_status launch_pair_t(const PairPlan& p, const CUtensorMap* tmX, const CUte
     while (args.acc_cols < p.bt * p.ctas) args.acc_cols *= 2;
     args.blocks = p.blocks;
     args.tiles_m = p.tiles_m;
-    args.whole = (int)p.whole;
     args.tiles = (int)p.tiles;
-    args.sharers = p.sharers;
+    args.split = p.split;
+    if (p.split) {
+        args.flags = static_cast<uint64_t*>(workspace);
+        args.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.flag_bytes);
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -167,19 +164,15 @@ w4a16_status launch_pair_t(const PairPlan& p, const CUtensorMap* tmX, const CUte
         cudaGetLastError();
         return W4A16_ECUDA;
     }
-    if (p.sharers == 0) return W4A16_OK;
-    const int64_t warps = (p.tiles - p.whole) * p.ctas * ((p.bt * p.ctas + 15) / 16) * 4;
-    const int per = kPairReduceThreads / 32;
-    return launch_chained(pair_reduce_kernel<DGRAD>, dim3((unsigned)((warps + per - 1) / per)), kPairReduceThreads,
-                          stream, args, p.ctas, p.upt);
+    return W4A16_OK;
 }
 
 template <int BITS, bool DGRAD>
 w4a16_status launch_pair(const PairPlan& p, const CUtensorMap* tmX, const CUtensorMap* tmP, const PairArgs& args,
-                         cudaStream_t stream) {
-    if (p.tiles > kMaxDim) return W4A16_EINVAL;
-    return p.ctas == 2 ? launch_pair_t<true, BITS, DGRAD>(p, tmX, tmP, args, stream)
-                       : launch_pair_t<false, BITS, DGRAD>(p, tmX, tmP, args, stream);
+                         void* workspace, cudaStream_t stream) {
+    if (p.tiles > kMaxDim / (p.blocks + 1)) return W4A16_EINVAL;
+    return p.ctas == 2 ? launch_pair_t<true, BITS, DGRAD>(p, tmX, tmP, args, workspace, stream)
+                       : launch_pair_t<false, BITS, DGRAD>(p, tmX, tmP, args, workspace, stream);
 }
 
 struct Weights {
@@ -223,12 +216,12 @@ w4a16_status launch_dgrad(const PairPlan& p, const void* const* dY, const Weight
     PairArgs a{};
     fill_weight_args(&a, w, products, K, g, sym, bits);
     a.out = static_cast<uint16_t*>(dX);
-    a.partials = static_cast<float*>(parts);
     a.M = (int)M;
     a.N = (int)N;
     a.K = (int)K;
     a.products = products;
-    return bits == 8 ? launch_pair<8, true>(p, tmX, tmP, a, stream) : launch_pair<4, true>(p, tmX, tmP, a, stream);
+    return bits == 8 ? launch_pair<8, true>(p, tmX, tmP, a, parts, stream)
+                     : launch_pair<4, true>(p, tmX, tmP, a, parts, stream);
 }
 
 PairPlan dgrad_plan(int64_t M, int64_t N, int64_t K, int products) {
@@ -404,13 +397,13 @@ w4a16_status gated_impl(const void* X, int64_t M, int64_t K, const Weights* w, i
     a.out = static_cast<uint16_t*>(H);
     a.G = static_cast<uint16_t*>(G);
     a.U = static_cast<uint16_t*>(U);
-    a.partials = static_cast<float*>(workspace);
     a.M = (int)M;
     a.N = (int)N;
     a.K = (int)K;
     a.act = act;
     a.products = 1;
-    return bits == 8 ? launch_pair<8, false>(q.p, tmX, tmP, a, s) : launch_pair<4, false>(q.p, tmX, tmP, a, s);
+    return bits == 8 ? launch_pair<8, false>(q.p, tmX, tmP, a, workspace, s)
+                     : launch_pair<4, false>(q.p, tmX, tmP, a, workspace, s);
 }
 
 size_t gated_ws(int64_t M, int64_t N, int64_t K, int32_t g, int32_t path, int bits) {

@@ -26,8 +26,8 @@
 // tensor core reads as the transposed A operand; nothing is transposed in memory.
 //
 // Warps: 0 loads tokens (TMA, 128-byte swizzle), 2 loads codes (TMA), 1 issues the MMAs
-// and owns the tensor memory, 4..11 dequantize and run the epilogue (eight, so that a
-// thread has up to 168 registers; sixteen warps of 96 spilled and were slower).  Three rings of
+// and owns the tensor memory, 4 and up dequantize and run the epilogue (8 or 12, so that a
+// thread has 168 or 128 registers; sixteen of 96 spilled and were slower).  Three rings of
 // shared memory, because the three have different sizes and lead times: token blocks,
 // code units (GATED with 4 bits: 128 input channels, so that a row is 64 bytes; loaded as
 // 32-byte rows the TMA engine's row rate, not bandwidth, paced the kernel) and dequantized
@@ -152,6 +152,17 @@ __device__ __forceinline__ void tc_commit_g(uint32_t bar) {
         tc_commit(bar);
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0u;
+}
+
 // Shared-memory descriptor of an MN-major operand in the 128-byte swizzle layout: lines
 // of 64 contiguous bf16 along M (or N), one line per step of K; groups of 8 lines are
 // 1024 bytes apart, the next 64 along M (or N) lie `block_bytes` further.
@@ -169,27 +180,43 @@ constexpr uint32_t kIdescAMnMajor = 1u << 15;
 constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
 // ------------------------------------------------------------------ configuration
-constexpr int kPairDequantWarps = 8;     // warps 4 .. 11, in two groups of four
 constexpr int kPairCodeWarp = 2;
-constexpr int kPairThreads = (4 + kPairDequantWarps) * 32;
 constexpr int kPairBlock = 64;          // reduction per block
 constexpr int kPairRows = 128;          // rows of one A tile per CTA
 constexpr int kPairABytes = 2 * kPairRows * kPairBlock * 2;   // both A tiles of a block: 32 KB
-constexpr int kPairABufs = 3;
-constexpr int kPairStageBytes = kPairDequantWarps * 1024;     // epilogue staging, 1 KB per warp
-constexpr int kPairXBytes = 64 * 1024;                        // token ring
-constexpr int kPairPBytes = 48 * 1024;                        // code ring
 constexpr int kPairMaxX = 8;
-constexpr int kPairSmemBytes = kPairABufs * kPairABytes + kPairXBytes + kPairPBytes + kPairStageBytes + 1024 + 1024;
-static_assert(kPairSmemBytes <= 232448, "shared memory");
+constexpr int kPairMaxWarps = 12;       // dequantizing warps, at most
+
+// A pair's tiles keep the tensor cores busy longer than two groups of dequantizing warps
+// need for a block (0.54 us); a single CTA's small tiles do not (two groups took 0.61 us per
+// block at any token count), so it has a third group and a fourth A buffer for it, and
+// smaller rings of loads.
+template <bool PAIR>
+struct PairConfig {
+#ifndef NPG
+#define NPG 2
+#endif
+    static constexpr int kGroups = PAIR ? 2 : NPG;
+    static constexpr int kWarps = 4 * kGroups;                 // warps 4 .. 4 + kWarps - 1
+    static constexpr int kThreads = (4 + kWarps) * 32;
+    static constexpr int kABufs = PAIR ? 3 : NPG + 1;
+    static constexpr int kStage = kWarps * 1024;               // epilogue staging, 1 KB per warp
+    static constexpr int kLoads = PAIR || NPG == 2 ? 112 * 1024 : 84 * 1024;   // token and code rings
+    static constexpr int kSmem = kABufs * kPairABytes + kStage + kLoads + 1024 + 1024;
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+// Bytes of the code ring; the token ring has the rest of the loads' space.
+template <bool PAIR>
+__host__ __device__ constexpr int pair_code_ring(int bt) {
+    return PAIR || bt <= 64 ? 48 * 1024 : 32 * 1024;
+}
 
 // Blocks of 64 that one code unit covers, and its bytes.
 template <int BITS, bool DGRAD>
 struct PairUnit {
     static constexpr int kBlocks = (!DGRAD && BITS == 4) ? 2 : 1;
     static constexpr int kBytes = 2 * kPairRows * kPairBlock * BITS / 8 * kBlocks;
-    static constexpr int kSlots = kPairPBytes / kBytes;
-    static_assert(kSlots >= 3, "code ring");
 };
 
 struct PairArgs {
@@ -212,7 +239,7 @@ struct PairArgs {
     int tiles_m;
     int tiles;
     int split;                   // 1: the tiles' code units are divided evenly over the CTAs
-    uint64_t* flags;             // [slots][CTAs of a slot][8] ready flags of the parts
+    uint64_t* flags;             // [slots][CTAs of a slot][12] ready flags of the parts
 };
 
 // Ready flag of a part: no sum, index or bf16 data is likely to hold it, so the workspace
@@ -470,7 +497,7 @@ struct PairTileDone {
 // The epilogue of one warp: its strips of the accumulators, finished or left as a part.
 template <bool PAIR, bool DGRAD>
 __device__ __forceinline__ bool pair_epilogue(const PairArgs& a, const PairTileDone& t, int rank, int w) {
-    constexpr int kCtas = PAIR ? 2 : 1;
+    constexpr int kCtas = PAIR ? 2 : 1, kGroups = PairConfig<PAIR>::kGroups;
     const int lane = threadIdx.x & 31;
     const int mma_n = kCtas * a.bt;
     bool ok = mbar_wait_cluster(t.accf, t.phase);
@@ -481,11 +508,11 @@ __device__ __forceinline__ bool pair_epilogue(const PairArgs& a, const PairTileD
     const uint32_t t_lane = t.tmem + ((uint32_t)(quarter * 32) << 16);
     const int64_t part_floats = pair_part_floats(mma_n);
     for (int c = t.slot + 1; c < t.followers_end && ok; ++c)
-        ok = pair_wait_flag(a.flags + ((int64_t)c * kCtas + rank) * kPairDequantWarps + w);
+        ok = pair_wait_flag(a.flags + ((int64_t)c * kCtas + rank) * kPairMaxWarps + w);
     if (!__all_sync(0xffffffffu, ok ? 1 : 0)) return false;
-    // strips of this warp: the quarter's strips are dealt over its two warps
+    // strips of this warp: the quarter's strips are dealt over its warps
 #pragma unroll 1
-    for (int sidx = w >> 2; sidx < strips; sidx += kPairDequantWarps / 4) {
+    for (int sidx = w >> 2; sidx < strips; sidx += kGroups) {
         uint32_t v0[16], v1[16];
         const uint32_t t0 = t_lane + 16 * sidx;
         tmem_ld_16x256b_x2(t0, v0);
@@ -493,7 +520,7 @@ __device__ __forceinline__ bool pair_epilogue(const PairArgs& a, const PairTileD
         tmem_ld_16x256b_x2(t0 + a.acc_cols, v1);
         tmem_ld_16x256b_x2(t0 + a.acc_cols + (16u << 16), v1 + 8);
         tmem_wait_ld();
-        if (sidx + kPairDequantWarps / 4 >= strips) {
+        if (sidx + kGroups >= strips) {
             // the last of them is in registers: the next tile may have the accumulators
             tc_fence_before();
             __syncwarp();
@@ -540,41 +567,43 @@ __device__ __forceinline__ bool pair_epilogue(const PairArgs& a, const PairTileD
         __threadfence();                               // every lane's part before the flag
         __syncwarp();
         if (lane == 0)
-            st_release_u64(a.flags + ((int64_t)t.slot * kCtas + rank) * kPairDequantWarps + w, kPairFlagReady);
+            st_release_u64(a.flags + ((int64_t)t.slot * kCtas + rank) * kPairMaxWarps + w, kPairFlagReady);
     } else if (t.followers_end > t.slot + 1) {
         __syncwarp();
         if (lane == 0)                                 // the parts were read: their flags are free again
             for (int c = t.slot + 1; c < t.followers_end; ++c)
-                a.flags[((int64_t)c * kCtas + rank) * kPairDequantWarps + w] = 0ull;
+                a.flags[((int64_t)c * kCtas + rank) * kPairMaxWarps + w] = 0ull;
     }
     return true;
 }
 
 template <bool PAIR, int BITS, bool DGRAD>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(PairConfig<PAIR>::kThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmX0, const __grid_constant__ CUtensorMap tmX1,
                      const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmP1,
                      const __grid_constant__ PairArgs a) {
     using Unit = PairUnit<BITS, DGRAD>;
-    constexpr int UB = Unit::kBlocks, SP = Unit::kSlots, NA = kPairABufs;
+    using Cfg = PairConfig<PAIR>;
+    constexpr int UB = Unit::kBlocks, NA = Cfg::kABufs, NG = Cfg::kGroups;
     constexpr int kCtas = PAIR ? 2 : 1;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int p_ring = pair_code_ring<PAIR>(a.bt), x_bytes = a.bt * kPairBlock * 2;
+    const int SP = min(p_ring / Unit::kBytes, kPairMaxX);             // code units
+    const int SX = min((Cfg::kLoads - p_ring) / x_bytes, kPairMaxX);  // token blocks
     const uint32_t as = smem_u32(smem);              // NA x kPairABytes
-    const uint32_t xs = as + NA * kPairABytes;       // token ring: SX x bt x 128 bytes
-    const uint32_t ps = xs + kPairXBytes;            // SP code units
-    const uint32_t st = ps + kPairPBytes;            // epilogue staging
-    const uint32_t bars = st + kPairStageBytes;
-    const int x_bytes = a.bt * kPairBlock * 2;
-    const int SX = min(kPairXBytes / x_bytes, kPairMaxX);
+    const uint32_t ps = as + NA * kPairABytes;       // code ring
+    const uint32_t xs = ps + p_ring;                 // token ring
+    const uint32_t st = ps + Cfg::kLoads;            // epilogue staging
+    const uint32_t bars = st + Cfg::kStage;
     const uint32_t xfull = bars, xempty = xfull + 8 * kPairMaxX;
-    const uint32_t pfull = xempty + 8 * kPairMaxX, pempty = pfull + 8 * SP;
-    const uint32_t afull = pempty + 8 * SP, aempty = afull + 8 * NA;
+    const uint32_t pfull = xempty + 8 * kPairMaxX, pempty = pfull + 8 * kPairMaxX;
+    const uint32_t afull = pempty + 8 * kPairMaxX, aempty = afull + 8 * NA;
     const uint32_t accf = aempty + 8 * NA, accempty = accf + 8;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + (accempty + 8 - as));
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
     const int slots = (int)gridDim.x / kCtas, slot = (int)blockIdx.x / kCtas;
@@ -588,14 +617,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         for (int s = 0; s < SP; ++s) {
             mbar_init(pfull + 8 * s, 1);
-            mbar_init(pempty + 8 * s, UB * kPairDequantWarps / 2);
+            mbar_init(pempty + 8 * s, 4 * UB);
         }
         for (int s = 0; s < NA; ++s) {
-            mbar_init(afull + 8 * s, kCtas * kPairDequantWarps / 2);
+            mbar_init(afull + 8 * s, kCtas * 4);
             mbar_init(aempty + 8 * s, 1);
         }
         mbar_init(accf, 1);
-        mbar_init(accempty, kCtas * kPairDequantWarps);
+        mbar_init(accempty, kCtas * Cfg::kWarps);
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
@@ -684,8 +713,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issue (even CTA)
-        if (lane == 0 && rank == 0) {
+        // The whole warp runs the loop and one elected lane issues, so that the descriptors
+        // live in uniform registers: formed in one lane's registers, eight MMAs took 1100
+        // cycles to issue beside busy dequantizing warps, more than they take to run.
+        if (rank == 0) {
             const uint32_t idesc = idesc_bf16_f32(kCtas * kPairRows, mma_n) | (DGRAD ? kIdescAMnMajor : 0u);
+            const uint64_t ad0 = DGRAD ? sw128_mnmajor_desc(as, 8192) : sw128_kmajor_desc(as);
+            const uint64_t bd0 = sw128_kmajor_desc(xs);
+            constexpr uint32_t kStepA = DGRAD ? 2048 / 16 : 32 / 16;     // 16 of the reduction, in 16-byte units
+            const uint32_t acc1 = tmem_d + (uint32_t)a.acc_cols;
             int s = 0, ab = 0, seg = 0;
             uint32_t pa = 0;
             bool ok = true;
@@ -699,33 +735,32 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     ok = mbar_wait_cluster(afull + 8 * ab, pa);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t at = as + ab * kPairABytes, xt = xs + s * x_bytes;
+                    const uint64_t ad = ad0 + (uint32_t)(ab * (kPairABytes / 16));
+                    const uint64_t bd = bd0 + (uint32_t)(s * (x_bytes / 16));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kPairBlock / 16; ++kk) {
-                        const uint64_t bd = sw128_kmajor_desc(xt + kk * 32);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint32_t aj = at + j * (kPairABytes / 2);
-                            const uint64_t ad = DGRAD ? sw128_mnmajor_desc(aj + kk * 2048, 8192)
-                                                      : sw128_kmajor_desc(aj + kk * 32);
-                            tc_mma_bf16_g<PAIR>(tmem_d + (uint32_t)(j * a.acc_cols), ad, bd, idesc,
-                                                (i | kk) != 0 ? 1u : 0u);
+                        for (int kk = 0; kk < kPairBlock / 16; ++kk) {
+                            const uint32_t acc = (i | kk) != 0 ? 1u : 0u;
+                            tc_mma_bf16_g<PAIR>(tmem_d, ad + kk * kStepA, bd + kk * 2, idesc, acc);
+                            tc_mma_bf16_g<PAIR>(acc1, ad + (kPairABytes / 32 + kk * kStepA), bd + kk * 2, idesc, acc);
                         }
+                        tc_commit_g<PAIR>(xempty + 8 * s);
+                        tc_commit_g<PAIR>(aempty + 8 * ab);
+                        if (i == nb - 1) tc_commit_g<PAIR>(accf);
                     }
-                    tc_commit_g<PAIR>(xempty + 8 * s);
-                    tc_commit_g<PAIR>(aempty + 8 * ab);
+                    __syncwarp();
                     if (++s == SX) s = 0;
                     if (++ab == NA) { ab = 0; pa ^= 1u; }
                 }
-                tc_commit_g<PAIR>(accf);         // also on the error path: no MMA outlives the CTA
             }
+            if (!ok && elect_one()) tc_commit_g<PAIR>(accf);     // error: no MMA outlives the CTA
         }
         __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ dequantize, epilogue
-        // Two groups of four warps take the blocks in turn, so that one group's waits, fences
-        // and loads hide behind the other's arithmetic and each warp pays its per-block
-        // overhead for sixteen chunks of codes.
+        // Groups of four warps take the blocks in turn, so that one group's waits, fences and
+        // loads hide behind the others' arithmetic and each warp pays its per-block overhead
+        // for sixteen chunks of codes.
         const int w = warp - 4, grp = w >> 2, wg = w & 3;
         const bool sym = a.flip != 0u;
         const uint32_t afull_r = PAIR ? mapa_u32(afull, 0) : afull;
@@ -761,7 +796,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // this group's first block in each ring: slot and phase
             int ab = (cnt + grp) % NA, xslot = (cnt + grp) % SX;
             uint32_t aph = (uint32_t)((cnt + grp) / NA) & 1u, xph = (uint32_t)((cnt + grp) / SX) & 1u;
-            const int ufirst = ucnt + (UB == 2 ? 0 : grp);
+            const int ufirst = ucnt + grp / UB;
             int pslot = ufirst % SP;
             uint32_t pph = (uint32_t)(ufirst / SP) & 1u;
             cnt += nb;
@@ -769,6 +804,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // The A tiles of a block are written: visible to the tensor core, then counted; the
             // codes were used, so their slot is given back.  (Given back right behind the
             // loads, a slot was seen refilled before a load of it had been performed.)
+            int i = grp;
             auto release = [&]() {
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -778,15 +814,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     if constexpr (PAIR) mbar_arrive_cluster(afull_r + 8 * ab);
                     else mbar_arrive(afull + 8 * ab);
                     mbar_arrive(pempty + 8 * pslot);
+                    // (a segment's last unit may have one block: its second arrival)
+                    if (UB == 2 && i == nb - 1 && (i & 1) == 0) mbar_arrive(pempty + 8 * pslot);
                 }
-                xslot += 2;
-                if (xslot >= SX) { xslot -= SX; xph ^= 1u; }
-                ab += 2;
+                xslot += NG;
+                while (xslot >= SX) { xslot -= SX; xph ^= 1u; }
+                ab += NG;
                 if (ab >= NA) { ab -= NA; aph ^= 1u; }
-                pslot += UB == 2 ? 1 : 2;
-                if (pslot >= SP) { pslot -= SP; pph ^= 1u; }
+                pslot += UB == 2 ? (NG == 2 ? 1 : 1 + (i & 1)) : NG;
+                while (pslot >= SP) { pslot -= SP; pph ^= 1u; }
             };
-            int i = grp;
             if constexpr (!DGRAD) {
                 // thread = row r of both matrices
                 const int r = wg * 32 + lane;
@@ -795,8 +832,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const bool vec = (a.groups & 3) == 0;         // rows of scales are 8-byte aligned
                 const int64_t srow = (int64_t)n * a.groups;
                 const uint32_t sts0 = (uint32_t)(r * 128 + ((r & 7) * 16));               // chunk c: ^ 16·c
-                const uint32_t lds0 = ps + (uint32_t)(r * 64) +
-                                      (uint32_t)(((BITS == 4 ? 2 * grp : 0) ^ ((r >> 1) & 3)) * 16);
+                const uint32_t lds0 = ps + (uint32_t)(r * 64 + ((r >> 1) & 3) * 16);      // chunk c: ^ 16·c
                 auto group_of = [&](int blk, int h) {
                     return min(((b0 + blk) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
                 };
@@ -824,16 +860,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 };
                 // first block of this warp whose scales lie behind those at hand
                 auto beyond = [&](int blk) {
-                    if (!vec) return blk + 2;
+                    if (!vec) return blk + NG;
                     const int k = ((((group_of(blk, 0) >> 2) + 1) * 4) << a.gshift) / kPairBlock - b0;
-                    return max(blk + 2, k + ((k ^ grp) & 1));
+                    return max(blk + NG, k + (grp - k % NG + NG) % NG);
                 };
 #pragma unroll
                 for (int j = 0; j < 2; ++j) cur[0][j] = cur[1][j] = nxt[0][j] = nxt[1][j] = make_uint2(0u, 0u);
                 if (more) fetch(nxt, grp);
                 for (int phase = pending ? 0 : 1; phase < 2; ++phase) {
                     const int hi = phase == 0 ? min(nb, NA) : nb;
-                    for (; i < hi && ok; i += 2) {
+                    for (; i < hi && ok; i += NG) {
                         const int ga = group_of(i, 0), gb = group_of(i, 1);
                         if (ga != have || gb != ga) {
                             if (!vec || have < 0 || (ga >> 2) != (have >> 2)) {
@@ -856,16 +892,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             }
                             have = ga;
                         }
+                        // (the A slot first: once it is free, the code slot's previous unit was used,
+                        // so the phase awaited next is not mistaken for an older one)
+                        ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
                         ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
+                        if (!ok) break;
                         uint4 v[2][BITS / 2];
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
 #pragma unroll
                             for (int c = 0; c < BITS / 2; ++c)
                                 v[j][c] = lds128_addr((lds0 + (uint32_t)(pslot * Unit::kBytes + j * (Unit::kBytes / 2))) ^
-                                                      (uint32_t)(16 * c));
-                        ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
-                        if (!ok) break;
+                                                      (uint32_t)(16 * c + (UB == 2 ? 32 * (i & 1) : 0)));
                         const uint32_t arow = as + (uint32_t)(ab * kPairABytes) + sts0;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -887,11 +925,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         release();
                     }
                     if (phase == 0 && ok) epilogue();
-                }
-                if (UB == 2 && ok && grp == 1 && (nb & 1)) {
-                    // the segment's last unit has no block for this group
-                    ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
-                    if (lane == 0) mbar_arrive(pempty + 8 * pslot);
                 }
             } else {
                 // thread = weight row r of the block, 128 channels (one A tile) q: a warp's scale
@@ -924,13 +957,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 for (int t = 0; t < 4; ++t) sa[t] = za[t] = sn[t] = zn[t] = 0u;
                 if (more) {
                     fetch(grp, sa, za);
-                    fetch(grp + 2, sn, zn);
+                    fetch(grp + NG, sn, zn);
                 }
                 const uint32_t row = ps + (uint32_t)(r * 128 + (BITS == 8 ? q * (kPairBlock * 128) : 0));
                 const uint32_t line = as + (uint32_t)(q * (kPairABytes / 2) + r * 128 + (((4 * q) ^ (r & 7)) * 16));
                 for (int phase = pending ? 0 : 1; phase < 2; ++phase) {
                     const int hi = phase == 0 ? min(nb, NA) : nb;
-                    for (; i < hi && ok; i += 2) {
+                    for (; i < hi && ok; i += NG) {
                         uint32_t sc[4], zc[4];                   // pairs of the four 32-channel pieces
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {
@@ -944,15 +977,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                             sa[t] = sn[t];
                             za[t] = zn[t];
                         }
-                        fetch(i + 4, sn, zn);
+                        fetch(i + 2 * NG, sn, zn);
+                        ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;       // first, as above
                         ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
+                        if (!ok) break;
                         const uint32_t prow = row + (uint32_t)(pslot * Unit::kBytes);
                         uint4 v[BITS];                           // the thread's codes
 #pragma unroll
                         for (int c = 0; c < BITS; ++c)
                             v[c] = lds128_addr(prow + (uint32_t)((((BITS == 4 ? 4 * q : 0) + c) ^ (r & 7)) * 16));
-                        ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;
-                        if (!ok) break;
                         const uint32_t aline = line + (uint32_t)(ab * kPairABytes);
 #pragma unroll
                         for (int b = 0; b < 2; ++b) {            // blocks of 64 channels

@@ -79,9 +79,12 @@ struct PairPlan {
 // 256 for a pair, in steps of 16.
 //
 // Split: whole tiles in waves leave CTAs idle in the last one.  Dividing all units evenly
-// ends that, and costs each CTA writing one part and reading one.  Both times are
-// estimated and the smaller taken: a block takes about 0.6 us per 256 tokens and at least
-// 0.22 us (dequantization), a CTA moves a part at about 80 GB/s, and 2 us go to the flags.
+// ends that, and costs each CTA writing a part and reading one, and the sharing of
+// operands in L2 between CTAs that work side by side.  Waves that are three quarters full are
+// left whole (M = 2048, 64 and 344 tiles on 74 pairs: 292 and 274 us whole, 306 and 284 us
+// split; 16 tiles: 285 us whole, 101 us split); below that both times are estimated: a block
+// takes about 0.55 us per 256 tokens and at least 0.3 us (dequantization), a CTA moves a part
+// at about 80 GB/s, and 2 us go to the flags.
 PairPlan pair_plan(int64_t M, int64_t rows, int rows_per_cta, int64_t blocks, int unit_blocks, int sm_count) {
     PairPlan p{};
     p.ctas = M > 128 ? 2 : 1;
@@ -97,15 +100,16 @@ PairPlan pair_plan(int64_t M, int64_t rows, int rows_per_cta, int64_t blocks, in
     p.grid = (int)(p.tiles < slots ? p.tiles : slots);
     int64_t sharers = p.tiles * units / 2;             // two units at least for each
     if (sharers > slots) sharers = slots;
-    if (sharers > p.grid || p.tiles % slots != 0) {
+    const int64_t waves = (p.tiles + slots - 1) / slots;
+    if (4 * p.tiles < 3 * waves * slots) {
         const int64_t part = pair_part_floats((int)tokens) * 4;
-        const double block_us = tokens * 0.6 / 256 > 0.22 ? tokens * 0.6 / 256 : 0.22;
-        const double whole = (double)((p.tiles + slots - 1) / slots) * blocks * block_us;
+        const double block_us = tokens * 0.55 / 256 > 0.3 ? tokens * 0.55 / 256 : 0.3;
+        const double whole = (double)waves * blocks * block_us;
         const double split = (double)p.tiles * blocks * block_us / (double)sharers + 2.0 + 2.0 * part / 80e3;
         if (sharers >= p.grid && split < whole) {
             p.split = 1;
             p.grid = (int)sharers;
-            p.flag_bytes = round256(sharers * p.ctas * kPairDequantWarps * 8);
+            p.flag_bytes = round256(sharers * p.ctas * kPairMaxWarps * 8);
             p.bytes = p.flag_bytes + sharers * p.ctas * part;
         }
     }
@@ -135,7 +139,7 @@ w4a16_status launch_pair_t(const PairPlan& p, const CUtensorMap* tmX, const CUte
                            void* workspace, cudaStream_t stream) {
     auto kern = gemm_pair_kernel<PAIR, BITS, DGRAD>;
     static bool done[kMaxDevices] = {};
-    w4a16_status st = set_smem(kern, kPairSmemBytes, done);
+    w4a16_status st = set_smem(kern, PairConfig<PAIR>::kSmem, done);
     if (st != W4A16_OK) return st;
     args.bt = p.bt;
     args.acc_cols = 32;
@@ -155,8 +159,8 @@ w4a16_status launch_pair_t(const PairPlan& p, const CUtensorMap* tmX, const CUte
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.grid * p.ctas), 1, 1);
-    cfg.blockDim = dim3(kPairThreads, 1, 1);
-    cfg.dynamicSmemBytes = kPairSmemBytes;
+    cfg.blockDim = dim3(PairConfig<PAIR>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = PairConfig<PAIR>::kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 1 : 0;

@@ -6,17 +6,20 @@
 // a warp reads 128 (256) contiguous code bytes and writes 512 contiguous bytes.
 //
 // Gradient:  dW[v, :] = scale·Σ_{t: id_t = v} dY[t, :], summed in binary32 in ascending t
-// within windows of kGradWindow sorted tokens, windows added in order: the same inputs
+// within windows of 32 or 64 sorted tokens (by T alone), windows added in order: the same inputs
 // give the same bits.  Four steps, no atomics on values:
-//   1. chunks of kSortChunk ids are sorted by (id, t) in shared memory, one bit of the id
-//      per pass (each pass a stable split), one CTA per chunk;
+//   1. chunks of ids are sorted by (id, t) in shared memory, one CTA per chunk: stable radix
+//      passes of five bits (the 32 digits are a warp's lanes, so counts live in registers);
 //   2. with more than one chunk, each element's place among the other chunks is found by
 //      binary search: its rank in the whole sorted list;
-//   3. windows of kGradWindow sorted tokens are summed, one thread per 8 columns; runs of one
+//   3. windows of 32 or 64 sorted tokens are summed, one thread per 8 columns; runs of one
 //      id inside a window are written at once, runs that cross its border leave a
-//      binary32 part; rows of the table that no token names are set to zero by the same
-//      launch, which is what most of its time goes to;
+//      binary32 part;
 //   4. parts of a run are added in window order and written.
+// Most of the time goes to writing zeros into the rows that no token names.  Step 3 writes
+// most of them (it finds them in the sorted list); the first 30 MB are written beside the
+// sort, which leaves the machine idle (by CTAs that look through the ids themselves), the
+// last sixteenth beside step 4.
 // An id below 0 or not below V names no row: it sorts behind all others and is dropped.
 #pragma once
 
@@ -97,83 +100,141 @@ __global__ void __launch_bounds__(256) embedding_kernel(const void* __restrict__
 }
 
 // ------------------------------------------------------------------ gradient
-constexpr int kSortThreads = 1024;
-constexpr int kSortPer = 4;
-constexpr int kSortChunk = kSortThreads * kSortPer;
-constexpr int kGradWindow = 32;                  // sorted tokens per window
+constexpr int kGradWindow = 64;                  // sorted tokens per window, at most
 constexpr int kGradThreads = 128;
 constexpr int kGradCols = kGradThreads * 8;      // columns per CTA
-constexpr int kZeroRows = 32;                    // table rows per zeroing CTA
+constexpr int kZeroRows = 8;                     // table rows per zeroing CTA
 
-// Step 1.  skey / sidx: [chunks][kSortChunk].
-__global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const void* __restrict__ ids, int wide,
-                                                                  int64_t T, int64_t V, int key_bits,
-                                                                  uint32_t* __restrict__ skey,
-                                                                  uint32_t* __restrict__ sidx) {
-    __shared__ uint32_t key_s[kSortChunk];
-    __shared__ uint16_t idx_s[kSortChunk];
-    __shared__ int warp_zeros[32];
-    grid_launch_dependents();
+// Step 1.  PER ids per thread; W holds id << IB | place in the chunk (IB bits), so one word
+// moves per pass.  skey / sidx: [chunks][THREADS·PER].  CTAs behind the chunks' zero rows
+// [0, zero_end), `zero_rows_per` each.
+template <typename W, int THREADS, int PER>
+struct SortConfig {
+    static constexpr int kChunk = THREADS * PER;
+    static constexpr int kWarps = THREADS / 32;
+    static constexpr int kIndexBits = kChunk == 1024 ? 10 : 14;
+    static_assert(kChunk <= 1 << kIndexBits && THREADS % 32 == 0 && THREADS <= 1024, "chunk");
+    static constexpr int kSmem = kChunk * (int)sizeof(W) + 32 * 33 * 4 + 32 * 4;
+};
+
+template <bool F32, int THREADS>
+__device__ __forceinline__ void zero_rows_by_ids(const void* ids, int wide, int64_t T, int64_t v0, int64_t v1, int K,
+                                                 void* __restrict__ dW, uint32_t* mask, int mask_words) {
+    for (int i = threadIdx.x; i < mask_words; i += THREADS) mask[i] = 0u;
+    __syncthreads();
+    for (int64_t t0 = threadIdx.x; t0 < T; t0 += 8 * THREADS) {
+        int64_t id[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) id[j] = t0 + j * THREADS < T ? load_id(ids, wide, t0 + j * THREADS) : -1;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (id[j] >= v0 && id[j] < v1) atomicOr(&mask[(id[j] - v0) >> 5], 1u << ((id[j] - v0) & 31));
+    }
+    __syncthreads();
+    const int row16 = K * (F32 ? 4 : 2) / 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int64_t v = v0 + warp; v < v1; v += THREADS / 32) {
+        if ((mask[(v - v0) >> 5] >> ((v - v0) & 31)) & 1u) continue;
+        uint4* o = static_cast<uint4*>(dW) + v * row16;
+        for (int c = lane; c < row16; c += 32) o[c] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+template <typename W, int THREADS, int PER, bool F32>
+__global__ void __launch_bounds__(THREADS) embed_sort_kernel(const void* __restrict__ ids, int wide, int64_t T,
+                                                             int64_t V, int key_bits, uint32_t* __restrict__ skey,
+                                                             uint32_t* __restrict__ sidx, int chunks,
+                                                             int64_t zero_end, int zero_rows_per, int K,
+                                                             void* __restrict__ dW) {
+    using Cfg = SortConfig<W, THREADS, PER>;
+    constexpr int IB = Cfg::kIndexBits;
+    extern __shared__ __align__(16) uint8_t sort_smem[];
+    W* word_s = reinterpret_cast<W*>(sort_smem);
+    int* hist = reinterpret_cast<int*>(sort_smem + Cfg::kChunk * sizeof(W));      // [digit][33] by warp
+    int* total = hist + 32 * 33;
+    if ((int)blockIdx.x >= chunks) {
+        const int64_t v0 = (int64_t)((int)blockIdx.x - chunks) * zero_rows_per;
+        const int64_t v1 = v0 + zero_rows_per < zero_end ? v0 + zero_rows_per : zero_end;
+        zero_rows_by_ids<F32, THREADS>(ids, wide, T, v0, v1, K, dW, reinterpret_cast<uint32_t*>(sort_smem),
+                                       (zero_rows_per + 31) / 32);
+        return;
+    }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int64_t base = (int64_t)blockIdx.x * kSortChunk;
-    uint32_t key[kSortPer];
-    uint32_t idx[kSortPer];
+    const int64_t base = (int64_t)blockIdx.x * Cfg::kChunk;
+    const uint32_t below = (1u << lane) - 1u;
+    W word[PER];
     // element order: warp, then item, then lane
 #pragma unroll
-    for (int i = 0; i < kSortPer; ++i) {
-        const int p = warp * 32 * kSortPer + i * 32 + lane;
+    for (int i = 0; i < PER; ++i) {
+        const int p = warp * 32 * PER + i * 32 + lane;
         const int64_t t = base + p;
-        key[i] = (uint32_t)V;
-        idx[i] = (uint32_t)p;
+        W key = (W)V;
         if (t < T) {
             const int64_t id = load_id(ids, wide, t);
-            if (id >= 0 && id < V) key[i] = (uint32_t)id;
+            if (id >= 0 && id < V) key = (W)id;
             else if (id >= V) report_error(kErrBadId);
         }
+        word[i] = key << IB | (W)p;
     }
-    for (int b = 0; b < key_bits; ++b) {
-        uint32_t ball[kSortPer];
-        int zeros = 0;
+    for (int b = 0; b < key_bits; b += 5) {
+        // this warp's elements of each digit (counted by the lane of that number), and each
+        // element's rank among them
+        int count = 0;
+        uint32_t rank[PER / 2];                  // two 16-bit ranks a word
 #pragma unroll
-        for (int i = 0; i < kSortPer; ++i) {
-            ball[i] = __ballot_sync(0xffffffffu, ((key[i] >> b) & 1u) == 0u);
-            zeros += __popc(ball[i]);
+        for (int i = 0; i < PER; ++i) {
+            const uint32_t d = (uint32_t)(word[i] >> (IB + b)) & 31u;
+            uint32_t mine = 0xffffffffu, counted = 0xffffffffu;
+#pragma unroll
+            for (int k = 0; k < 5; ++k) {
+                const uint32_t v = __ballot_sync(0xffffffffu, (d >> k) & 1u);
+                mine &= (d >> k) & 1u ? v : ~v;
+                counted &= (lane >> k) & 1 ? v : ~v;
+            }
+            const uint32_t r = (uint32_t)(__shfl_sync(0xffffffffu, count, d) + __popc(mine & below));
+            if (i & 1) rank[i >> 1] |= r << 16;
+            else rank[i >> 1] = r;
+            count += __popc(counted);
         }
-        if (lane == 0) warp_zeros[warp] = zeros;
+        hist[lane * 33 + warp] = count;
         __syncthreads();
-        const int mine = warp_zeros[lane];
-        int incl = mine;
+        // a warp per digit: its elements in the warps before each warp
+        for (int d = warp; d < 32; d += Cfg::kWarps) {
+            const int c = lane < Cfg::kWarps ? hist[d * 33 + lane] : 0;
+            int incl = c;
+#pragma unroll
+            for (int o = 1; o < Cfg::kWarps; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            if (lane < Cfg::kWarps) hist[d * 33 + lane] = incl - c;
+            if (lane == Cfg::kWarps - 1) total[d] = incl;
+        }
+        __syncthreads();
+        const int tot = total[lane];
+        int dincl = tot;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+            const int v = __shfl_up_sync(0xffffffffu, dincl, o);
+            if (lane >= o) dincl += v;
         }
-        const int total = __shfl_sync(0xffffffffu, incl, 31);
-        int z = __shfl_sync(0xffffffffu, incl - mine, warp);       // zeros before this warp
-        int ones = total + warp * 32 * kSortPer - z;               // ones go behind all zeros
-        const uint32_t below = (1u << lane) - 1u;
+        const int start = dincl - tot + hist[lane * 33 + warp];      // of digit `lane`, this warp
 #pragma unroll
-        for (int i = 0; i < kSortPer; ++i) {
-            const int zb = __popc(ball[i] & below);
-            const int at = (ball[i] >> lane) & 1u ? z + zb : ones + lane - zb;
-            key_s[at] = key[i];
-            idx_s[at] = (uint16_t)idx[i];
-            z += __popc(ball[i]);
-            ones += 32 - __popc(ball[i]);
+        for (int i = 0; i < PER; ++i) {
+            const uint32_t d = (uint32_t)(word[i] >> (IB + b)) & 31u;
+            const int at = __shfl_sync(0xffffffffu, start, d) + (int)((rank[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+            word_s[at] = word[i];
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kSortPer; ++i) {
-            const int p = warp * 32 * kSortPer + i * 32 + lane;
-            key[i] = key_s[p];
-            idx[i] = idx_s[p];
-        }
+        for (int i = 0; i < PER; ++i) word[i] = word_s[warp * 32 * PER + i * 32 + lane];
+        // (the next pass writes word_s only after its first barrier, behind these reads)
     }
 #pragma unroll
-    for (int i = 0; i < kSortPer; ++i) {
-        const int64_t p = base + warp * 32 * kSortPer + i * 32 + lane;
-        skey[p] = key[i];
-        sidx[p] = (uint32_t)(base + idx[i]);
+    for (int i = 0; i < PER; ++i) {
+        const int64_t p = base + warp * 32 * PER + i * 32 + lane;
+        skey[p] = (uint32_t)(word[i] >> IB);
+        sidx[p] = (uint32_t)(base + (int64_t)(word[i] & (W)((1 << IB) - 1)));
     }
 }
 
@@ -200,30 +261,65 @@ __device__ __forceinline__ int64_t lower_bound_u32(const uint32_t* key, int64_t 
     return lo;
 }
 
-// Step 2.  `lanes` threads (a power of two up to 32) per element, each searching chunks
-// lane, lane + lanes, ...: equal ids of earlier chunks come first.
-__global__ void __launch_bounds__(256) embed_rank_kernel(const uint32_t* __restrict__ skey,
-                                                         const uint32_t* __restrict__ sidx, int chunks,
-                                                         int lanes, uint32_t* __restrict__ key,
-                                                         uint32_t* __restrict__ idx) {
-    grid_launch_dependents();
+// Step 2.  An element's rank is its place in its chunk plus, for every other chunk, the number
+// of smaller ids there (of ids not larger, in the chunks before its own: equal ids keep
+// their order).  SHARED: all chunks' keys are brought into shared memory first, four threads per
+// element; else `lanes` threads (a power of two up to 32) per element search in L2.
+constexpr int kRankThreads = 512;
+constexpr int kRankPer = 4;                     // threads per element of the shared form
+constexpr int64_t kRankShared = 16384;          // ids, at most, for the shared form
+
+template <bool SHARED>
+__global__ void __launch_bounds__(kRankThreads) embed_rank_kernel(const uint32_t* __restrict__ skey,
+                                                                  const uint32_t* __restrict__ sidx, int chunks,
+                                                                  int chunk, int lanes, uint32_t* __restrict__ key,
+                                                                  uint32_t* __restrict__ idx) {
+    extern __shared__ __align__(16) uint32_t rank_smem[];
     grid_dependency_wait();
-    const int64_t total = (int64_t)chunks * kSortChunk;
-    const int64_t e = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lanes;
-    if (e >= total) return;                                  // whole groups of `lanes` leave together
-    const int sub = threadIdx.x % lanes;
-    const int own = (int)(e / kSortChunk);
-    const uint32_t k = ld_u32(skey + e);
-    int64_t rank = 0;
-    for (int c = sub; c < chunks; c += lanes)
-        if (c != own)
-            rank += lower_bound_u32(skey + (int64_t)c * kSortChunk, kSortChunk, c < own ? k + 1u : k);
-    const uint32_t group = lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << ((threadIdx.x & 31) / lanes * lanes);
-    for (int o = lanes >> 1; o > 0; o >>= 1) rank += __shfl_xor_sync(group, rank, o);
-    if (sub == 0) {
-        rank += e - (int64_t)own * kSortChunk;
-        key[rank] = k;
-        idx[rank] = ld_u32(sidx + e);
+    const int64_t total = (int64_t)chunks * chunk;
+    if constexpr (SHARED) {
+#pragma unroll 8
+        for (int i = threadIdx.x; i < (int)total / 4; i += kRankThreads)
+            reinterpret_cast<uint4*>(rank_smem)[i] = __ldcg(reinterpret_cast<const uint4*>(skey) + i);
+        __syncthreads();
+        const int e = (int)blockIdx.x * (kRankThreads / kRankPer) + threadIdx.x / kRankPer;   // < total: see the launch
+        const int sub = threadIdx.x % kRankPer;
+        const uint32_t k = rank_smem[e];
+        const int own = e / chunk;
+        int rank = 0;
+        for (int c = sub; c < chunks; c += kRankPer) {
+            if (c == own) continue;
+            const uint32_t v = c < own ? k + 1u : k;
+            const uint32_t* p = rank_smem + c * chunk;
+            int lo = 0;                              // chunk is a power of two
+            for (int half = chunk >> 1; half > 0; half >>= 1)
+                if (p[lo + half - 1] < v) lo += half;
+            rank += lo + (p[lo] < v ? 1 : 0);
+        }
+#pragma unroll
+        for (int o = kRankPer >> 1; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+        if (sub == 0) {
+            rank += e - own * chunk;
+            key[rank] = k;
+            idx[rank] = ld_u32(sidx + e);
+        }
+    } else {
+        const int64_t e = ((int64_t)blockIdx.x * kRankThreads + threadIdx.x) / lanes;
+        if (e >= total) return;                                  // whole groups of `lanes` leave together
+        const int sub = threadIdx.x % lanes;
+        const int own = (int)(e / chunk);
+        const uint32_t k = ld_u32(skey + e);
+        int64_t rank = 0;
+        for (int c = sub; c < chunks; c += lanes)
+            if (c != own) rank += lower_bound_u32(skey + (int64_t)c * chunk, chunk, c < own ? k + 1u : k);
+        const uint32_t group =
+            lanes == 32 ? 0xffffffffu : ((1u << lanes) - 1u) << ((threadIdx.x & 31) / lanes * lanes);
+        for (int o = lanes >> 1; o > 0; o >>= 1) rank += __shfl_xor_sync(group, rank, o);
+        if (sub == 0) {
+            rank += e - (int64_t)own * chunk;
+            key[rank] = k;
+            idx[rank] = ld_u32(sidx + e);
+        }
     }
 }
 
@@ -242,31 +338,79 @@ __device__ __forceinline__ void grad_write(void* dW, int64_t at, const float v[8
     }
 }
 
-// Step 3.  CTAs [0, windows·slices) sum windows, the rest zero the rows that no token
-// names.  part: [windows][2][K] binary32 (slot 0: a run that began before the window,
-// slot 1: a run that goes on behind it).
+// lower_bound_u32 by a warp: 32 probes a step instead of one.
+__device__ __forceinline__ int64_t lower_bound_warp(const uint32_t* key, int64_t n, uint32_t v) {
+    const int lane = threadIdx.x & 31;
+    int64_t lo = 0;
+    while (n > 0) {
+        // probes divide the range into 33 parts (into single elements when it is short)
+        const int64_t step = n / 33 + 1;
+        const int64_t p = (lane + 1) * step - 1;
+        const int less = __popc(__ballot_sync(0xffffffffu, p < n && ld_u32(key + lo + p) < v));
+        // the first `less` probes are below v: the bound lies behind probe less − 1 and not
+        // behind probe `less`
+        const int64_t from = less * step, to = (less + 1) * step - 1;
+        lo += from;
+        n = (to < n ? to : n) - from;
+    }
+    return lo;
+}
+
+// Sets the rows v0 .. v0 + kZeroRows - 1 of the table that no token names to zero.
+template <bool F32>
+__device__ __forceinline__ void zero_rows(const uint32_t* key, int64_t padded, int64_t v0, int64_t V, int K,
+                                          void* __restrict__ dW, uint32_t* present) {
+    const int tid = threadIdx.x;
+    const int rows = (int)(V - v0 < kZeroRows ? V - v0 : kZeroRows);
+    if (tid < 32) {
+        const int64_t lo = lower_bound_warp(key, padded, (uint32_t)v0);
+        uint32_t mask = 0u;
+        // most often the next 32 keys reach behind the rows; a long run is searched past
+        if (tid < rows) {
+            const uint32_t v = (uint32_t)(v0 + tid);
+            int64_t p = lo;
+            for (int j = 0; j < 32 && p < padded && ld_u32(key + p) < v; ++j) ++p;
+            if (p < padded && ld_u32(key + p) < v) p += lower_bound_u32(key + p, padded - p, v);
+            if (p < padded && ld_u32(key + p) == v) mask = 1u << tid;
+        }
+        mask = __reduce_or_sync(0xffffffffu, mask);
+        if (tid == 0) *present = mask;
+    }
+    __syncthreads();
+    const uint32_t mask = *present;
+    const int row16 = K * (F32 ? 4 : 2) / 16;                   // K is a multiple of 32
+    uint4* o = static_cast<uint4*>(dW) + v0 * row16;
+    for (int r = 0; r < rows; ++r) {
+        if ((mask >> r) & 1u) continue;
+        for (int c = tid; c < row16; c += kGradThreads) o[(int64_t)r * row16 + c] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// Step 3.  CTAs [0, windows·slices) sum windows, the rest zero rows [zero_begin, zero_end).  part:
+// [windows][2][K] binary32 (slot 0: a run that began before the window, slot 1: a run that
+// goes on behind it).
 template <bool F32>
 __global__ void __launch_bounds__(kGradThreads) embed_grad_kernel(const uint16_t* __restrict__ dY,
                                                                   const uint32_t* __restrict__ key,
                                                                   const uint32_t* __restrict__ idx,
-                                                                  int64_t padded, int windows, int slices,
-                                                                  int64_t V, int K, float scale,
-                                                                  void* __restrict__ dW,
+                                                                  int64_t padded, int window, int windows, int slices,
+                                                                  int64_t V, int64_t zero_begin,
+                                                                  int64_t zero_end, int K,
+                                                                  float scale, void* __restrict__ dW,
                                                                   float* __restrict__ part) {
     __shared__ uint32_t ks[kGradWindow + 2];
     __shared__ uint32_t is[kGradWindow];
     __shared__ uint32_t present;
-    grid_launch_dependents();
     grid_dependency_wait();
     const int tid = threadIdx.x;
     if ((int64_t)blockIdx.x < (int64_t)windows * slices) {
         const int w = (int)(blockIdx.x / slices), slice = (int)(blockIdx.x % slices);
-        const int64_t p0 = (int64_t)w * kGradWindow;
-        if (tid < kGradWindow + 2) {
+        const int64_t p0 = (int64_t)w * window;
+        if (tid < window + 2) {
             const int64_t p = p0 + tid - 1;
             ks[tid] = p >= 0 && p < padded ? ld_u32(key + p) : 0xffffffffu;
         }
-        if (tid < kGradWindow) is[tid] = ld_u32(idx + p0 + tid);
+        if (tid < window) is[tid] = ld_u32(idx + p0 + tid);
         __syncthreads();
         const int col = slice * kGradCols + tid * 8;
         if (col >= K) return;
@@ -275,7 +419,7 @@ __global__ void __launch_bounds__(kGradThreads) embed_grad_kernel(const uint16_t
         for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
         bool began = ks[0] == ks[1];                 // the first run began in an earlier window
 #pragma unroll 1
-        for (int j0 = 0; j0 < kGradWindow; j0 += 8) {
+        for (int j0 = 0; j0 < window; j0 += 8) {
             uint4 v[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -291,7 +435,7 @@ __global__ void __launch_bounds__(kGradThreads) embed_grad_kernel(const uint16_t
                     acc[2 * i] += __uint_as_float(q[i] << 16);
                     acc[2 * i + 1] += __uint_as_float(q[i] & 0xFFFF0000u);
                 }
-                const bool last = j0 + j == kGradWindow - 1;
+                const bool last = j0 + j == window - 1;
                 const bool on = ks[2 + j0 + j] == k;         // the run goes on behind this token
                 if (on && !last) continue;
                 if (began || on) {
@@ -308,54 +452,62 @@ __global__ void __launch_bounds__(kGradThreads) embed_grad_kernel(const uint16_t
         }
         return;
     }
-    // zeroing: a mask of the rows that tokens name, from the sorted list
-    const int64_t v0 = ((int64_t)blockIdx.x - (int64_t)windows * slices) * kZeroRows;
-    const int rows = (int)(V - v0 < kZeroRows ? V - v0 : kZeroRows);
-    if (tid == 0) present = 0u;
-    __syncthreads();
-    if (tid < rows) {
-        const int64_t p = lower_bound_u32(key, padded, (uint32_t)(v0 + tid));
-        if (p < padded && ld_u32(key + p) == (uint32_t)(v0 + tid)) atomicOr(&present, 1u << tid);
-    }
-    __syncthreads();
-    const uint32_t mask = present;
-    const int row16 = K * (F32 ? 4 : 2) / 16;                   // K is a multiple of 8
-    uint4* o = static_cast<uint4*>(dW) + v0 * row16;
-    for (int r = 0; r < rows; ++r) {
-        if ((mask >> r) & 1u) continue;
-        for (int c = tid; c < row16; c += kGradThreads) o[(int64_t)r * row16 + c] = make_uint4(0, 0, 0, 0);
-    }
+    zero_rows<F32>(key, padded, zero_begin + ((int64_t)blockIdx.x - (int64_t)windows * slices) * kZeroRows, zero_end, K, dW,
+                   &present);
 }
 
-// Step 4.  One CTA per window whose last run goes on behind it and begins in it.
+// Step 4.  One CTA per window and slice, at work when the window's last run begins in it and
+// goes on behind it; the CTAs behind them zero rows [zero_begin, V).
 template <bool F32>
 __global__ void __launch_bounds__(kGradThreads) embed_grad_join_kernel(const uint32_t* __restrict__ key,
-                                                                       int64_t padded, int windows, int64_t V,
-                                                                       int K, float scale,
-                                                                       void* __restrict__ dW,
+                                                                       int64_t padded, int window, int windows, int slices,
+                                                                       int64_t V, int64_t zero_begin, int K,
+                                                                       float scale, void* __restrict__ dW,
                                                                        const float* __restrict__ part) {
+    __shared__ uint32_t present;
     grid_dependency_wait();
-    const int w = (int)blockIdx.x;
-    const int64_t end = (int64_t)(w + 1) * kGradWindow;         // first place behind the window
+    if ((int64_t)blockIdx.x >= (int64_t)windows * slices) {
+        zero_rows<F32>(key, padded, zero_begin + ((int64_t)blockIdx.x - (int64_t)windows * slices) * kZeroRows, V, K, dW,
+                       &present);
+        return;
+    }
+    const int w = (int)(blockIdx.x / slices);
+    const int64_t end = (int64_t)(w + 1) * window;         // first place behind the window
     if (end >= padded) return;
-    const uint32_t k = ld_u32(key + end - 1);
-    if ((int64_t)k >= V || ld_u32(key + end) != k) return;               // no run crosses this border
-    // the window holds the run's beginning, unless the run fills it and began before
-    if (w > 0 && ld_u32(key + end - kGradWindow) == k && ld_u32(key + end - kGradWindow - 1) == k) return;
-    const int col = (int)blockIdx.y * kGradCols + threadIdx.x * 8;
+    const uint32_t k = ld_u32(key + end - 1), behind = ld_u32(key + end), first = ld_u32(key + end - window);
+    const uint32_t before = w > 0 ? ld_u32(key + end - window - 1) : 0xffffffffu;
+    // no run crosses this border, or the run fills the window and began before it
+    if ((int64_t)k >= V || behind != k || (first == k && before == k)) return;
+    // windows w + 1 .. w1 begin inside the run: a warp looks at the first keys of 32 windows
+    int w1 = w;
+    for (int j0 = w + 1;; j0 += 32) {
+        const int64_t p = (int64_t)(j0 + (threadIdx.x & 31)) * window;
+        const uint32_t on = __ballot_sync(0xffffffffu, p < padded && ld_u32(key + p) == k);
+        const int run = __ffs(~on) - 1;                       // -1: all 32
+        w1 = j0 + (run < 0 ? 32 : run) - 1;
+        if (run >= 0) break;
+    }
+    const int col = (int)(blockIdx.x % slices) * kGradCols + threadIdx.x * 8;
     if (col >= K) return;
-    // windows w + 1 .. w1 begin inside the run
-    const int64_t last = lower_bound_u32(key + end, padded - end, k + 1u) + end - 1;
-    const int w1 = (int)(last / kGradWindow);
     float acc[8];
     const float* p = part + ((int64_t)w * 2 + 1) * K + col;
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = __ldcg(p + i);
-    for (int j = w + 1; j <= w1; ++j) {
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(part + (int64_t)j * 2 * K + col));
-        const float4 b = __ldcg(reinterpret_cast<const float4*>(part + (int64_t)j * 2 * K + col + 4));
-        acc[0] += a.x; acc[1] += a.y; acc[2] += a.z; acc[3] += a.w;
-        acc[4] += b.x; acc[5] += b.y; acc[6] += b.z; acc[7] += b.w;
+    for (int j0 = w + 1; j0 <= w1; j0 += 8) {
+        // eight windows' loads in flight, then their sums in order
+        float4 a[8], b[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float* q = part + (int64_t)min(j0 + j, w1) * 2 * K + col;
+            a[j] = __ldcg(reinterpret_cast<const float4*>(q));
+            b[j] = __ldcg(reinterpret_cast<const float4*>(q + 4));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j0 + j > w1) break;
+            acc[0] += a[j].x; acc[1] += a[j].y; acc[2] += a[j].z; acc[3] += a[j].w;
+            acc[4] += b[j].x; acc[5] += b[j].y; acc[6] += b[j].z; acc[7] += b[j].w;
+        }
     }
     grad_write<F32>(dW, (int64_t)k * K + col, acc, scale);
 }

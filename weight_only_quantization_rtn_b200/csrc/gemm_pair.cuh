@@ -14,7 +14,7 @@
 // 128 x 256 tile with one accumulator uses up (loads, dequantized stores and operand
 // reads together), has room left.
 //
-// PAIR (more than 128 tokens): two CTAs of a cluster compute one tile together
+// PAIR (more than 96 tokens): two CTAs of a cluster compute one tile together
 // (cta_group::2): each holds its own 128 rows of both A tiles and half of the tokens, one
 // thread of the even CTA issues the MMAs (M = 256) for both, and each SM reads half of
 // the B operand.  The token tile is the batch divided evenly (at most 256 tokens), in
@@ -187,29 +187,32 @@ constexpr int kPairABytes = 2 * kPairRows * kPairBlock * 2;   // both A tiles of
 constexpr int kPairMaxX = 8;
 constexpr int kPairMaxWarps = 12;       // dequantizing warps, at most
 
-// A pair's tiles keep the tensor cores busy longer than two groups of dequantizing warps
-// need for a block (0.54 us); a single CTA's small tiles do not (two groups took 0.61 us per
-// block at any token count), so it has a third group and a fourth A buffer for it, and
-// smaller rings of loads.
-template <bool PAIR>
+// A pair's MMAs take longer than two groups of dequantizing warps need for a block; a single
+// CTA's small tiles do not, so it has a third group and a fourth A buffer for it, and smaller
+// rings of loads (M = 61, K = 8192, N = 18944: 84.7 us with two groups, 79.6 us with three;
+// the gradient with M = 77, K = 37888, N = 8192: 157 and 133 us).  With 8-bit codes, whose
+// units are larger, a third group gained nothing (102 us both).
+template <bool PAIR, int BITS>
 struct PairConfig {
-#ifndef NPG
-#define NPG 2
-#endif
-    static constexpr int kGroups = PAIR ? 2 : NPG;
+    static constexpr int kGroups = !PAIR && BITS == 4 ? 3 : 2;
     static constexpr int kWarps = 4 * kGroups;                 // warps 4 .. 4 + kWarps - 1
     static constexpr int kThreads = (4 + kWarps) * 32;
-    static constexpr int kABufs = PAIR ? 3 : NPG + 1;
+    static constexpr int kABufs = kGroups + 1;
     static constexpr int kStage = kWarps * 1024;               // epilogue staging, 1 KB per warp
-    static constexpr int kLoads = PAIR || NPG == 2 ? 112 * 1024 : 84 * 1024;   // token and code rings
+    static constexpr int kLoads = kGroups == 2 ? 112 * 1024 : 84 * 1024;   // token and code rings
     static constexpr int kSmem = kABufs * kPairABytes + kStage + kLoads + 1024 + 1024;
     static_assert(kSmem <= 232448, "shared memory");
 };
 
-// Bytes of the code ring; the token ring has the rest of the loads' space.
-template <bool PAIR>
+// Most tokens of a tile of one CTA: its token ring must hold a block for each A buffer.
+constexpr int kPairMaxSingle = 96;
+
+// Bytes of the code ring; the token ring has the rest of the loads' space.  Both rings hold
+// at least kABufs blocks, so that a free A slot implies that what their slots held before was
+// used: a warp that awaits a slot's next phase cannot be looking at an older one.
+template <int GROUPS>
 __host__ __device__ constexpr int pair_code_ring(int bt) {
-    return PAIR || bt <= 64 ? 48 * 1024 : 32 * 1024;
+    return GROUPS == 2 || bt <= 64 ? 48 * 1024 : 32 * 1024;
 }
 
 // Blocks of 64 that one code unit covers, and its bytes.
@@ -495,9 +498,9 @@ struct PairTileDone {
 };
 
 // The epilogue of one warp: its strips of the accumulators, finished or left as a part.
-template <bool PAIR, bool DGRAD>
+template <bool PAIR, int GROUPS, bool DGRAD>
 __device__ __forceinline__ bool pair_epilogue(const PairArgs& a, const PairTileDone& t, int rank, int w) {
-    constexpr int kCtas = PAIR ? 2 : 1, kGroups = PairConfig<PAIR>::kGroups;
+    constexpr int kCtas = PAIR ? 2 : 1, kGroups = GROUPS;
     const int lane = threadIdx.x & 31;
     const int mma_n = kCtas * a.bt;
     bool ok = mbar_wait_cluster(t.accf, t.phase);
@@ -578,18 +581,18 @@ __device__ __forceinline__ bool pair_epilogue(const PairArgs& a, const PairTileD
 }
 
 template <bool PAIR, int BITS, bool DGRAD>
-__global__ void __launch_bounds__(PairConfig<PAIR>::kThreads, 1)
+__global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmX0, const __grid_constant__ CUtensorMap tmX1,
                      const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmP1,
                      const __grid_constant__ PairArgs a) {
     using Unit = PairUnit<BITS, DGRAD>;
-    using Cfg = PairConfig<PAIR>;
+    using Cfg = PairConfig<PAIR, BITS>;
     constexpr int UB = Unit::kBlocks, NA = Cfg::kABufs, NG = Cfg::kGroups;
     constexpr int kCtas = PAIR ? 2 : 1;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int p_ring = pair_code_ring<PAIR>(a.bt), x_bytes = a.bt * kPairBlock * 2;
+    const int p_ring = pair_code_ring<NG>(a.bt), x_bytes = a.bt * kPairBlock * 2;
     const int SP = min(p_ring / Unit::kBytes, kPairMaxX);             // code units
     const int SX = min((Cfg::kLoads - p_ring) / x_bytes, kPairMaxX);  // token blocks
     const uint32_t as = smem_u32(smem);              // NA x kPairABytes
@@ -784,7 +787,7 @@ __global__ void __launch_bounds__(PairConfig<PAIR>::kThreads, 1)
             t.accempty = PAIR ? mapa_u32(accempty, 0) : accempty;
             t.tmem = tmem_d;
             t.stage = st + w * 1024;
-            ok = pair_epilogue<PAIR, DGRAD>(a, t, rank, w);
+            ok = pair_epilogue<PAIR, NG, DGRAD>(a, t, rank, w);
             ++seg;
         };
 

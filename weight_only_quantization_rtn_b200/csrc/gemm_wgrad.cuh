@@ -9,7 +9,9 @@
 // 256 x 256 tile (cta_group::2: each SM holds 128 rows of dYᵀ and half of X's columns, and
 // reads half of the B operand).  The kernel is persistent, one pair per two SMs, with two
 // accumulators in tensor memory, so that one tile's epilogue overlaps the next one's
-// MMAs: a tile of 2048 tokens is only about 9 us of MMAs.
+// MMAs: a tile of 2048 tokens is only about 9 us of MMAs.  A warp's 32 rows x 64 channels leave
+// through shared memory as one TMA store of full 128-byte lines (a lane writing its own row
+// in 16-byte pieces took 65 us for M = 77, N = K = 8192, where writing dW is all there is to do).
 #pragma once
 
 #include "gemm_pair.cuh"
@@ -22,22 +24,25 @@ constexpr int kWgBlockM = 64;                    // tokens per stage
 constexpr int kWgTile = 256;                     // features x channels per pair
 constexpr int kWgStageBytes = 2 * 128 * kWgBlockM * 2;   // A and B halves of one CTA: 32 KB
 constexpr int kWgStages = 6;
-constexpr int kWgSmemBytes = kWgStages * kWgStageBytes + 1024 + 1024;
+constexpr int kWgOutBytes = kWgEpiWarps * 4096;           // a warp's 32 rows x 64 channels
+constexpr int kWgSmemBytes = kWgStages * kWgStageBytes + kWgOutBytes + 1024 + 1024;
+static_assert(kWgSmemBytes <= 232448, "shared memory");
 
 __global__ void __launch_bounds__(kWgThreads, 1)
     gemm_wgrad_kernel(const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmX,
-                      uint16_t* __restrict__ dW, int M, int N, int K) {
+                      const __grid_constant__ CUtensorMap tmW, int M, int N, int K) {
     constexpr int S = kWgStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * kWgStageBytes);
+    uint8_t* outs = smem + S * kWgStageBytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(outs + kWgOutBytes);
     uint64_t* pfull = full + S;          // the odd CTA's stage has landed (at the even CTA)
     uint64_t* empty = pfull + S;
     uint64_t* accf = empty + S;          // [2] accumulator complete
     uint64_t* acce = accf + 2;           // [2] accumulator drained by both CTAs (at the even CTA)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acce + 2);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
     const int pairs = (int)gridDim.x / 2, pair = (int)blockIdx.x / 2;
@@ -99,67 +104,82 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                     ok = mbar_wait(smem_u32(&full[i % S]), (uint32_t)(i / S) & 1u);
                     if (ok) mbar_arrive_cluster(mapa_u32(smem_u32(&pfull[i % S]), 0));
                 }
-        } else if (lane == 0) {
+        } else if (rank == 0) {
+            // the whole warp runs the loop (descriptors in uniform registers), one lane issues
             constexpr uint32_t idesc = idesc_bf16_f32(256, 256) | kIdescAMnMajor | kIdescBMnMajor;
-            int i = 0, it = 0;
+            const uint64_t ad0 = sw128_mnmajor_desc(smem_u32(smem), 8192);
+            const uint64_t bd0 = sw128_mnmajor_desc(smem_u32(smem) + 16384, 8192);
+            int s = 0, it = 0;
+            uint32_t ph = 0;
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs, ++it) {
                 const int buf = it & 1;
                 ok = mbar_wait_cluster(smem_u32(&acce[buf]), ((uint32_t)(it >> 1) & 1u) ^ 1u);
                 if (!ok) break;
-                tc_fence_after();
-                for (int b = 0; b < nb; ++b, ++i) {
-                    const int s = i % S;
-                    const uint32_t ph = (uint32_t)(i / S) & 1u;
+                for (int b = 0; b < nb; ++b) {
                     ok = mbar_wait(smem_u32(&full[s]), ph) && mbar_wait_cluster(smem_u32(&pfull[s]), ph);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t st = smem_u32(smem + s * kWgStageBytes);
+                    const uint64_t ad = ad0 + (uint32_t)(s * (kWgStageBytes / 16)), bd = bd0 + (uint32_t)(s * (kWgStageBytes / 16));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kWgBlockM / 16; ++kk)
-                        tc_mma_bf16_g<true>(tmem_d + (uint32_t)(buf * 256),
-                                            sw128_mnmajor_desc(st + kk * 2048, 8192),
-                                            sw128_mnmajor_desc(st + 16384 + kk * 2048, 8192), idesc,
-                                            (b | kk) != 0 ? 1u : 0u);
-                    tc_commit_g<true>(smem_u32(&empty[s]));
+                        for (int kk = 0; kk < kWgBlockM / 16; ++kk)
+                            tc_mma_bf16_g<true>(tmem_d + (uint32_t)(buf * 256), ad + kk * 128, bd + kk * 128, idesc,
+                                                (b | kk) != 0 ? 1u : 0u);
+                        tc_commit_g<true>(smem_u32(&empty[s]));
+                        if (b == nb - 1) tc_commit_g<true>(smem_u32(&accf[buf]));
+                    }
+                    __syncwarp();
+                    if (++s == S) { s = 0; ph ^= 1u; }
                 }
-                tc_commit_g<true>(smem_u32(&accf[buf]));
             }
+            if (!ok && elect_one()) tc_commit_g<true>(smem_u32(&accf[it & 1]));   // error: no MMA outlives the CTA
         }
         __syncwarp();
     } else {
-        // epilogue: lane = feature row, 32 channels at a time
-        const int h = (warp - 2) >> 2;
-        const int r = (warp & 3) * 32 + lane;
+        // epilogue: lane = feature row, 64 channels at a time
+        const int h = (warp - 2) >> 2, quarter = warp & 3;
+        const uint32_t out = smem_u32(outs) + (uint32_t)((warp - 2) * 4096);
         int it = 0;
+        if (lane == 0) prefetch_tensormap(&tmW);
         for (int t = pair; t < tiles; t += pairs, ++it) {
             const int buf = it & 1;
-            const int n = (t % tiles_n) * kWgTile + rank * 128 + r, k0 = (t / tiles_n) * kWgTile;
+            const int n = (t % tiles_n) * kWgTile + rank * 128 + 32 * quarter, k0 = (t / tiles_n) * kWgTile;
             if (!mbar_wait_cluster(smem_u32(&accf[buf]), (uint32_t)(it >> 1) & 1u)) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int cb = h; cb < kWgTile / 32; cb += 2) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tmem_d + (uint32_t)(buf * 256 + cb * 32) + ((uint32_t)((warp & 3) * 32) << 16), v);
+            for (int cb = h; cb < kWgTile / 64; cb += 2) {
+                uint32_t v[64];
+                const uint32_t at = tmem_d + (uint32_t)(buf * 256 + cb * 64) + ((uint32_t)(quarter * 32) << 16);
+                tmem_ld_32x32b_x32(at, v);
+                tmem_ld_32x32b_x32(at + 32, v + 32);
                 tmem_wait_ld();
-                const int k = k0 + cb * 32;
-                if (n < N && k < K) {                         // K is a multiple of 32
-                    uint4* o = reinterpret_cast<uint4*>(dW + (int64_t)n * K + k);
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");   // staging is free
+                __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t p[4];
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t p[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[j])
-                                : "f"(__uint_as_float(v[8 * c + 2 * j + 1])), "f"(__uint_as_float(v[8 * c + 2 * j])));
-                        o[c] = make_uint4(p[0], p[1], p[2], p[3]);
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        p[j] = pack_bf16(__uint_as_float(v[8 * c + 2 * j]), __uint_as_float(v[8 * c + 2 * j + 1]));
+                    sts128_addr(out + (uint32_t)(lane * 128 + ((c ^ (lane & 7)) * 16)), p);
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                const int k = k0 + 64 * cb;
+                if (lane == 0 && n < N && k < K)
+                    asm volatile(
+                        "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                        "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(&tmW)),
+                        "r"(k), "r"(n), "r"(out)
+                        : "memory");
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(mapa_u32(smem_u32(&acce[buf]), 0));
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
     tc_fence_before();
     __syncwarp();

@@ -75,8 +75,8 @@ struct PairPlan {
 
 // `rows` output rows (features or input channels) in tiles of `rows_per_cta` per CTA.
 //
-// Token tile: the batch in equal tiles of at most 128 tokens for one CTA (one tile) and
-// 256 for a pair, in steps of 16.
+// Token tile: up to 96 tokens are one tile of a CTA each; more are divided evenly into tiles
+// of at most 256 for a pair, in steps of 16.
 //
 // Split: whole tiles in waves leave CTAs idle in the last one.  Dividing all units evenly
 // ends that, and costs each CTA writing a part and reading one, and the sharing of
@@ -87,8 +87,8 @@ struct PairPlan {
 // at about 80 GB/s, and 2 us go to the flags.
 PairPlan pair_plan(int64_t M, int64_t rows, int rows_per_cta, int64_t blocks, int unit_blocks, int sm_count) {
     PairPlan p{};
-    p.ctas = M > 128 ? 2 : 1;
-    const int64_t most = p.ctas == 2 ? 256 : 128;
+    p.ctas = M > kPairMaxSingle ? 2 : 1;
+    const int64_t most = p.ctas == 2 ? 256 : kPairMaxSingle;
     const int64_t tiles_m = (M + most - 1) / most;
     const int64_t tokens = tiles_m > 0 ? ((M + tiles_m - 1) / tiles_m + 15) / 16 * 16 : 16;
     p.bt = (int)(tokens / p.ctas);
@@ -117,13 +117,15 @@ PairPlan pair_plan(int64_t M, int64_t rows, int rows_per_cta, int64_t blocks, in
 }
 
 template <typename... A, typename... B>
-w4a16_status launch_chained(void (*kern)(A...), dim3 grid, int threads, cudaStream_t stream, B... args) {
+w4a16_status launch_chained(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                            B... args) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -139,7 +141,7 @@ w4a16_status launch_pair_t(const PairPlan& p, const CUtensorMap* tmX, const CUte
                            void* workspace, cudaStream_t stream) {
     auto kern = gemm_pair_kernel<PAIR, BITS, DGRAD>;
     static bool done[kMaxDevices] = {};
-    w4a16_status st = set_smem(kern, PairConfig<PAIR>::kSmem, done);
+    w4a16_status st = set_smem(kern, PairConfig<PAIR, BITS>::kSmem, done);
     if (st != W4A16_OK) return st;
     args.bt = p.bt;
     args.acc_cols = 32;
@@ -159,8 +161,8 @@ w4a16_status launch_pair_t(const PairPlan& p, const CUtensorMap* tmX, const CUte
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.grid * p.ctas), 1, 1);
-    cfg.blockDim = dim3(PairConfig<PAIR>::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = PairConfig<PAIR>::kSmem;
+    cfg.blockDim = dim3(PairConfig<PAIR, BITS>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = PairConfig<PAIR, BITS>::kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 1 : 0;
@@ -524,19 +526,45 @@ w4a16_status embedding_impl(const void* ids, int32_t id_bytes, int64_t T, const 
 // Workspace of the embedding gradient: chunk-sorted keys and tokens, the same merged
 // (more than one chunk), and the windows' binary32 parts.
 struct EmbedGradPlan {
-    int64_t chunks, padded, windows;
+    int key_bits;            // of the ids 0 .. V (V: dropped)
+    bool small;              // chunks of 1024 ids, else of 16384
+    int64_t chunk, chunks, padded;
+    int window;              // sorted tokens per window
+    int64_t windows;
     int64_t list_bytes;      // one key or token list
     int64_t bytes;
 };
 
-EmbedGradPlan embed_grad_plan(int64_t T, int64_t K) {
+// Chunks of 1024 ids spread the sort over many SMs (2048 ids in one CTA of 4096: 10 us, in two
+// of 1024: 4 us); ranking costs ids x chunks, so from 65536 ids on a chunk holds 16384.
+EmbedGradPlan embed_grad_plan(int64_t T, int64_t V, int64_t K) {
     EmbedGradPlan p{};
-    p.chunks = (T + kSortChunk - 1) / kSortChunk;
-    p.padded = p.chunks * kSortChunk;
-    p.windows = (T + kGradWindow - 1) / kGradWindow;
+    while (p.key_bits < 31 && (int64_t(1) << p.key_bits) <= V) ++p.key_bits;
+    p.small = T <= 65536;
+    p.chunk = p.small ? 1024 : 16384;
+    p.chunks = (T + p.chunk - 1) / p.chunk;
+    p.padded = p.chunks * p.chunk;
+    // (2048 ids: 37 us with 32, 42 with 64, which make half the CTAs; 16384 ids: joining the
+    // parts takes 23 us with 32 and 14 with 64)
+    p.window = T <= 4096 ? kGradWindow / 2 : kGradWindow;
+    p.windows = (T + p.window - 1) / p.window;
     p.list_bytes = p.padded * 4;
     p.bytes = p.list_bytes * (p.chunks > 1 ? 4 : 2) + p.windows * 2 * K * 4;
     return p;
+}
+
+template <typename W, int THREADS, int PER, bool F32>
+w4a16_status launch_sort(const EmbedGradPlan& p, const void* ids, int wide, int64_t T, int64_t V, uint32_t* skey,
+                         uint32_t* sidx, int64_t zero_end, int zero_ctas, int64_t K, void* dW, cudaStream_t s) {
+    using Cfg = SortConfig<W, THREADS, PER>;
+    auto kern = embed_sort_kernel<W, THREADS, PER, F32>;
+    static bool done[kMaxDevices] = {};
+    w4a16_status st = set_smem(kern, Cfg::kSmem, done);
+    if (st != W4A16_OK) return st;
+    const int per = zero_ctas > 0 ? (int)((zero_end + zero_ctas - 1) / zero_ctas) : 0;
+    kern<<<(unsigned)(p.chunks + zero_ctas), THREADS, Cfg::kSmem, s>>>(ids, wide, T, V, p.key_bits, skey, sidx,
+                                                                       (int)p.chunks, zero_end, per, (int)K, dW);
+    return launch_status();
 }
 
 bool embed_grad_ok(int64_t T, int64_t V, int64_t K) {
@@ -546,7 +574,7 @@ bool embed_grad_ok(int64_t T, int64_t V, int64_t K) {
 template <bool F32>
 w4a16_status launch_embed_grad(const void* dY, const void* ids, int wide, int64_t T, int64_t V, int64_t K, float scale,
                                void* dW, void* workspace, cudaStream_t s) {
-    const EmbedGradPlan p = embed_grad_plan(T, K);
+    const EmbedGradPlan p = embed_grad_plan(T, V, K);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     uint32_t* skey = reinterpret_cast<uint32_t*>(ws);
     uint32_t* sidx = reinterpret_cast<uint32_t*>(ws + p.list_bytes);
@@ -558,27 +586,44 @@ w4a16_status launch_embed_grad(const void* dY, const void* ids, int wide, int64_
         ws += 2 * p.list_bytes;
     }
     float* part = reinterpret_cast<float*>(ws);
-    int bits = 0;
-    while (bits < 31 && (int64_t(1) << bits) <= V) ++bits;        // keys 0 .. V
-    embed_sort_kernel<<<(unsigned)p.chunks, kSortThreads, 0, s>>>(ids, wide, T, V, bits, skey, sidx);
-    w4a16_status st = launch_status();
+    // Rows zeroed beside the sort: about 30 MB, what the machine writes in the sort's time.  Their
+    // CTAs look through all ids and keep a bit per row in shared memory (4 KB at least).
+    int64_t zero1 = T <= 16384 ? (int64_t)(30 << 20) / (K * (F32 ? 4 : 2)) : 0;
+    if (zero1 > V / 4) zero1 = V / 4;
+    const int zero_ctas = zero1 > 0 ? (int)(zero1 < 128 ? zero1 : 128) : 0;
+    if (zero1 > 128ll * 8 * 4096) zero1 = 128ll * 8 * 4096;
+    w4a16_status st;
+    if (p.small && p.key_bits <= 22)
+        st = launch_sort<uint32_t, 256, 4, F32>(p, ids, wide, T, V, skey, sidx, zero1, zero_ctas, K, dW, s);
+    else if (p.small)
+        st = launch_sort<uint64_t, 256, 4, F32>(p, ids, wide, T, V, skey, sidx, zero1, zero_ctas, K, dW, s);
+    else
+        st = launch_sort<uint64_t, 1024, 16, F32>(p, ids, wide, T, V, skey, sidx, zero1, zero_ctas, K, dW, s);
     if (st != W4A16_OK) return st;
     if (p.chunks > 1) {
         int lanes = 1;
         while (lanes < 32 && lanes < p.chunks) lanes *= 2;
-        const int64_t blocks = (p.padded * lanes + 255) / 256;
-        st = launch_chained(embed_rank_kernel, dim3((unsigned)blocks), 256, s, skey, sidx, (int)p.chunks, lanes, key, idx);
+        const bool shared = p.padded <= kRankShared;
+        // (whole blocks: padded is a multiple of 1024)
+        const int64_t blocks = shared ? p.padded * kRankPer / kRankThreads : p.padded * lanes / kRankThreads;
+        static bool done[kMaxDevices] = {};
+        if (shared && (st = set_smem(embed_rank_kernel<true>, (int)kRankShared * 4, done)) != W4A16_OK) return st;
+        st = launch_chained(shared ? embed_rank_kernel<true> : embed_rank_kernel<false>, dim3((unsigned)blocks),
+                            kRankThreads, shared ? (size_t)p.padded * 4 : 0, s, skey, sidx, (int)p.chunks,
+                            (int)p.chunk, lanes, key, idx);
         if (st != W4A16_OK) return st;
     }
     const int slices = (int)((K + kGradCols - 1) / kGradCols);
-    const int64_t blocks = p.windows * slices + (V + kZeroRows - 1) / kZeroRows;
-    if (blocks > kMaxDim) return W4A16_EINVAL;
-    st = launch_chained(embed_grad_kernel<F32>, dim3((unsigned)blocks), kGradThreads, s,
-                        static_cast<const uint16_t*>(dY), key, idx, p.padded, (int)p.windows, slices, V, (int)K, scale,
-                        dW, part);
+    const int64_t zero2 = zero1 + (V - zero1) * 15 / 16;
+    const int64_t blocks = p.windows * slices + (zero2 - zero1 + kZeroRows - 1) / kZeroRows;
+    const int64_t blocks2 = p.windows * slices + (V - zero2 + kZeroRows - 1) / kZeroRows;
+    if (blocks > kMaxDim || blocks2 > kMaxDim) return W4A16_EINVAL;
+    st = launch_chained(embed_grad_kernel<F32>, dim3((unsigned)blocks), kGradThreads, 0, s,
+                        static_cast<const uint16_t*>(dY), key, idx, p.padded, p.window, (int)p.windows, slices, V, zero1, zero2,
+                        (int)K, scale, dW, part);
     if (st != W4A16_OK) return st;
-    return launch_chained(embed_grad_join_kernel<F32>, dim3((unsigned)p.windows, (unsigned)slices), kGradThreads, s, key,
-                          p.padded, (int)p.windows, V, (int)K, scale, dW, part);
+    return launch_chained(embed_grad_join_kernel<F32>, dim3((unsigned)blocks2), kGradThreads, 0, s, key, p.padded,
+                          p.window, (int)p.windows, slices, V, zero2, (int)K, scale, dW, part);
 }
 
 }  // namespace
@@ -689,6 +734,10 @@ w4a16_status w4a16_gemm_wgrad(const void* dY, const void* X, int64_t M, int64_t 
     st = encode_rows(&tmX, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, X, (uint64_t)K, (uint64_t)M, (uint64_t)K * 2, 64, kWgBlockM,
                      CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != W4A16_OK) return st;
+    CUtensorMap tmW;
+    st = encode_rows(&tmW, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dW, (uint64_t)K, (uint64_t)N, (uint64_t)K * 2, 64, 32,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != W4A16_OK) return st;
     static bool done[kMaxDevices] = {};
     st = set_smem(gemm_wgrad_kernel, kWgSmemBytes, done);
     if (st != W4A16_OK) return st;
@@ -706,7 +755,7 @@ w4a16_status w4a16_gemm_wgrad(const void* dY, const void* X, int64_t M, int64_t 
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, gemm_wgrad_kernel, tmY, tmX, static_cast<uint16_t*>(dW), (int)M, (int)N, (int)K) !=
+    if (cudaLaunchKernelEx(&cfg, gemm_wgrad_kernel, tmY, tmX, tmW, (int)M, (int)N, (int)K) !=
         cudaSuccess) {
         cudaGetLastError();
         return W4A16_ECUDA;
@@ -728,7 +777,7 @@ w4a16_status w8a16_embedding(const void* ids, int32_t id_bytes, int64_t T, const
 
 size_t w4a16_embedding_grad_workspace_size(int64_t T, int64_t V, int64_t K) {
     if (!embed_grad_ok(T, V, K) || T == 0 || V == 0) return 0;
-    return (size_t)embed_grad_plan(T, K).bytes;
+    return (size_t)embed_grad_plan(T, V, K).bytes;
 }
 
 w4a16_status w4a16_embedding_grad(const void* dY, const void* ids, int32_t id_bytes, int64_t T, int64_t V, int64_t K,

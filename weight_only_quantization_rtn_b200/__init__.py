@@ -590,41 +590,70 @@ def device_error() -> int:
 
 
 # ---------------------------------------------------------------- gated block, gradients, embedding
+# These calls are often a few microseconds of GPU work, so their host side is kept short:
+# every check is made in one pass over cheap attributes, and the full checks above are run
+# only to name what is wrong.
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
+_BF16 = torch.bfloat16
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _sid(dev: torch.device) -> int:
+    """Handle of the current stream of a device."""
+    if _raw_stream is not None:
+        return _raw_stream(dev.index)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _act_id(act: str) -> int:
-    if act not in _ACTS:
+    aid = _ACTS.get(act)
+    if aid is None:
         raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
-    return _ACTS[act]
+    return aid
 
 
-def _weights(w, K: int | None, sym: bool, bits: int, name: str = ""):
-    """Checks a (codes, scales, zeros) triple and returns it with its N and K."""
+def _ok(t, dtype: torch.dtype, ndim: int) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.is_cuda
+            and t.is_contiguous())
+
+
+def _want(t, dtype: torch.dtype, name: str, ndim: int = 2) -> None:
+    if not _ok(t, dtype, ndim):
+        _need(t, dtype, name, ndim)
+
+
+def _weights(w, K: int | None, g: int, sym: bool, bits: int, name: str = ""):
+    """Checks a (codes, scales, zeros) triple; returns the tensors (zeros None when sym), N
+    and K."""
     codes, scales, zeros = w
-    _need(codes, torch.uint8, f"{name}codes" if bits == 8 else f"{name}packed")
-    _need(scales, torch.bfloat16, f"{name}scales")
-    if not sym:
-        _need(zeros, torch.bfloat16, f"{name}zeros")
-    N, kw = codes.shape[0], codes.shape[1] * (8 // bits)
+    _want(codes, torch.uint8, f"{name}codes" if bits == 8 else f"{name}packed")
+    _want(scales, _BF16, f"{name}scales")
+    N, kw = codes.shape
+    if bits == 4:
+        kw *= 2
     if K is not None and kw != K:
         raise ValueError(f"{name}weights have K={kw}, the activations have K={K}")
-    _same_device(codes.device, scales=scales, zeros=None if sym else zeros)
-    return codes, scales, None if sym else zeros, N, kw
+    groups = kw // g if g > 0 else 0
+    if scales.size(0) != N or scales.size(1) != groups:
+        raise ValueError(f"{name}scales must be [{N}, {groups}] for g={g}, got {list(scales.shape)}")
+    dev = codes.get_device()
+    if scales.get_device() != dev:
+        _same_device(codes.device, scales=scales)
+    if sym:
+        return codes, scales, None, N, kw
+    _want(zeros, _BF16, f"{name}zeros")
+    if zeros.size(0) != N or zeros.size(1) != groups:
+        raise ValueError(f"{name}zeros must be [{N}, {groups}] for g={g}, got {list(zeros.shape)}")
+    if zeros.get_device() != dev:
+        _same_device(codes.device, zeros=zeros)
+    return codes, scales, zeros, N, kw
 
 
-def _groups_ok(scales, zeros, N: int, K: int, g: int, name: str = "") -> None:
-    want = (N, K // g if g > 0 else 0)
-    for what, t in (("scales", scales), ("zeros", zeros)):
-        if t is not None and tuple(t.shape) != want:
-            raise ValueError(f"{name}{what} must be {list(want)} for g={g}, got {list(t.shape)}")
-
-
-def _result(out, shape, dtype, dev, name: str = "out") -> torch.Tensor:
+def _result(out, shape: tuple, dtype: torch.dtype, dev, name: str = "out") -> torch.Tensor:
     if out is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    _need(out, dtype, name, ndim=len(shape))
-    if tuple(out.shape) != tuple(shape):
+    _want(out, dtype, name, len(shape))
+    if tuple(out.shape) != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(out.shape)}")
     _same_device(dev, **{name: out})
     return out
@@ -632,6 +661,15 @@ def _result(out, shape, dtype, dev, name: str = "out") -> torch.Tensor:
 
 def _on(dev: torch.device):
     return torch.cuda.device(dev) if dev.index != torch.cuda.current_device() else _NO_CONTEXT
+
+
+def _scratch_bytes(name: str, dev: torch.device, *shape) -> int:
+    """What a *_workspace_size entry point says for a shape on a device, asked once."""
+    key = (name, dev.index, shape)
+    nbytes = _plan_bytes.get(key)
+    if nbytes is None:
+        nbytes = _plan_bytes[key] = int(getattr(lib(), name)(*shape))
+    return nbytes
 
 
 def _scratch(nbytes: int, dev: torch.device):
@@ -645,36 +683,31 @@ def _p(t):
 
 
 def _gated(X, gate, up, g, sym, act, out, save, path, static_weights, bits):
-    _need(X, torch.bfloat16, "X")
+    _want(X, _BF16, "X")
     M, K = X.shape
     sym = bool(sym)
-    gc, gs, gz, N, _ = _weights(gate, K, sym, bits, "gate ")
-    uc, us, uz, Nu, _ = _weights(up, K, sym, bits, "up ")
+    gc, gs, gz, N, _ = _weights(gate, K, g, sym, bits, "gate ")
+    uc, us, uz, Nu, _ = _weights(up, K, g, sym, bits, "up ")
     if Nu != N:
         raise ValueError(f"gate has {N} rows, up has {Nu}")
-    _groups_ok(gs, gz, N, K, g, "gate ")
-    _groups_ok(us, uz, N, K, g, "up ")
     dev = gc.device
-    _same_device(dev, X=X, up=uc)
+    if X.device != dev or uc.device != dev:
+        _same_device(dev, X=X, up=uc)
     aid = _act_id(act)
     pid = _PATHS[path] if isinstance(path, str) else int(path)
+    L = lib()
     with _on(dev):
-        H = _result(out, (M, N), torch.bfloat16, dev)
-        G = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if save else None
-        U = torch.empty((M, N), dtype=torch.bfloat16, device=dev) if save else None
-        L = lib()
-        key = ("gated", bits, dev.index, M, N, K, g, pid)
-        nbytes = _plan_bytes.get(key)
-        if nbytes is None:
-            size = L.w8a16_gated_workspace_size if bits == 8 else L.w4a16_gated_workspace_size
-            nbytes = _plan_bytes[key] = int(size(M, N, K, g, pid))
+        H = _result(out, (M, N), _BF16, dev)
+        G = torch.empty_like(H) if save else None
+        U = torch.empty_like(H) if save else None
+        nbytes = _scratch_bytes("w8a16_gated_workspace_size" if bits == 8 else "w4a16_gated_workspace_size",
+                                dev, M, N, K, g, pid)
         ws = _scratch(nbytes, dev)
         call = L.w8a16_gated if bits == 8 else L.w4a16_gated
-        _check(call(_p(X), M, K, _p(gc), _p(gs), _p(gz), _p(uc), _p(us), _p(uz), N, g, int(sym), aid,
-                    _p(H), _p(G), _p(U), _p(ws), nbytes,
-                    pid | (STATIC_WEIGHTS if static_weights else 0),
-                    torch.cuda.current_stream(dev).cuda_stream),
-               f"w{bits}a16_gated")
+        _check(call(X.data_ptr(), M, K, gc.data_ptr(), gs.data_ptr(), _p(gz), uc.data_ptr(),
+                    us.data_ptr(), _p(uz), N, g, sym, aid, H.data_ptr(), _p(G), _p(U), _p(ws), nbytes,
+                    pid | STATIC_WEIGHTS if static_weights else pid, _sid(dev)),
+               "w4a16_gated" if bits == 4 else "w8a16_gated")
     return (H, G, U) if save else H
 
 
@@ -699,33 +732,32 @@ def gated8(X: torch.Tensor, gate: tuple, up: tuple, g: int = 128, sym: bool = Fa
 
 
 def _gated_backward(dH, G, U, gate, up, g, sym, act, out, bits):
-    for name, t in (("dH", dH), ("G", G), ("U", U)):
-        _need(t, torch.bfloat16, name)
-    M, N = dH.shape
-    if tuple(G.shape) != (M, N) or tuple(U.shape) != (M, N):
+    _want(dH, _BF16, "dH")
+    _want(G, _BF16, "G")
+    _want(U, _BF16, "U")
+    M, N = shape = dH.shape
+    if G.shape != shape or U.shape != shape:
         raise ValueError("dH, G and U must have one shape")
     sym = bool(sym)
-    gc, gs, gz, Nw, K = _weights(gate, None, sym, bits, "gate ")
-    uc, us, uz, Nu, _ = _weights(up, K, sym, bits, "up ")
+    gc, gs, gz, Nw, K = _weights(gate, None, g, sym, bits, "gate ")
+    uc, us, uz, Nu, _ = _weights(up, K, g, sym, bits, "up ")
     if Nw != N or Nu != N:
         raise ValueError(f"dH has {N} columns, gate has {Nw} rows, up has {Nu}")
-    _groups_ok(gs, gz, N, K, g, "gate ")
-    _groups_ok(us, uz, N, K, g, "up ")
     dev = gc.device
-    _same_device(dev, dH=dH, G=G, U=U, up=uc)
+    if not dH.device == G.device == U.device == uc.device == dev:
+        _same_device(dev, dH=dH, G=G, U=U, up=uc)
     aid = _act_id(act)
+    L = lib()
     with _on(dev):
-        dX = _result(out, (M, K), torch.bfloat16, dev)
-        dG = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        dU = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-        L = lib()
-        nbytes = int(L.w4a16_gated_backward_workspace_size(M, N, K, g))
+        dX = _result(out, (M, K), _BF16, dev)
+        dG, dU = torch.empty_like(dH), torch.empty_like(dH)
+        nbytes = _scratch_bytes("w4a16_gated_backward_workspace_size", dev, M, N, K, g)
         ws = _scratch(nbytes, dev)
         call = L.w8a16_gated_backward if bits == 8 else L.w4a16_gated_backward
-        _check(call(_p(dH), _p(G), _p(U), M, N, _p(gc), _p(gs), _p(gz), _p(uc), _p(us), _p(uz), K, g,
-                    int(sym), aid, _p(dX), _p(dG), _p(dU), _p(ws), nbytes,
-                    torch.cuda.current_stream(dev).cuda_stream),
-               f"w{bits}a16_gated_backward")
+        _check(call(dH.data_ptr(), G.data_ptr(), U.data_ptr(), M, N, gc.data_ptr(), gs.data_ptr(), _p(gz),
+                    uc.data_ptr(), us.data_ptr(), _p(uz), K, g, sym, aid, dX.data_ptr(), dG.data_ptr(),
+                    dU.data_ptr(), _p(ws), nbytes, _sid(dev)),
+               "w4a16_gated_backward" if bits == 4 else "w8a16_gated_backward")
     return dX, dG, dU
 
 
@@ -749,24 +781,24 @@ def gated8_backward(dH: torch.Tensor, G: torch.Tensor, U: torch.Tensor, gate: tu
 
 
 def _dgrad(dY, w, g, sym, out, bits):
-    _need(dY, torch.bfloat16, "dY")
+    _want(dY, _BF16, "dY")
     M, N = dY.shape
     sym = bool(sym)
-    codes, scales, zeros, Nw, K = _weights(w, None, sym, bits)
+    codes, scales, zeros, Nw, K = _weights(w, None, g, sym, bits)
     if Nw != N:
         raise ValueError(f"dY has {N} columns, the weights have {Nw} rows")
-    _groups_ok(scales, zeros, N, K, g)
     dev = codes.device
-    _same_device(dev, dY=dY)
+    if dY.device != dev:
+        _same_device(dev, dY=dY)
+    L = lib()
     with _on(dev):
-        dX = _result(out, (M, K), torch.bfloat16, dev)
-        L = lib()
-        nbytes = int(L.w4a16_gemm_dgrad_workspace_size(M, N, K, g))
+        dX = _result(out, (M, K), _BF16, dev)
+        nbytes = _scratch_bytes("w4a16_gemm_dgrad_workspace_size", dev, M, N, K, g)
         ws = _scratch(nbytes, dev)
         call = L.w8a16_gemm_dgrad if bits == 8 else L.w4a16_gemm_dgrad
-        _check(call(_p(dY), M, N, _p(codes), _p(scales), _p(zeros), K, g, int(sym), _p(dX), _p(ws), nbytes,
-                    torch.cuda.current_stream(dev).cuda_stream),
-               f"w{bits}a16_gemm_dgrad")
+        _check(call(dY.data_ptr(), M, N, codes.data_ptr(), scales.data_ptr(), _p(zeros), K, g, sym,
+                    dX.data_ptr(), _p(ws), nbytes, _sid(dev)),
+               "w4a16_gemm_dgrad" if bits == 4 else "w8a16_gemm_dgrad")
     return dX
 
 
@@ -789,29 +821,29 @@ def gemm_wgrad(dY: torch.Tensor, X: torch.Tensor, out: torch.Tensor | None = Non
     """Gradient of a linear layer with respect to its dense weight: dW[N, K] =
     dY[M, N]ᵀ·X[M, K] (bf16, fp32 accumulation).  With weights quantized anew in every
     step it is the straight-through gradient of the weight that was quantized."""
-    _need(dY, torch.bfloat16, "dY")
-    _need(X, torch.bfloat16, "X")
+    _want(dY, _BF16, "dY")
+    _want(X, _BF16, "X")
     M, N = dY.shape
-    K = X.shape[1]
-    if X.shape[0] != M:
-        raise ValueError(f"dY has {M} rows, X has {X.shape[0]}")
+    Mx, K = X.shape
+    if Mx != M:
+        raise ValueError(f"dY has {M} rows, X has {Mx}")
     dev = X.device
     if dY.device != dev:
         raise ValueError(f"dY is on {dY.device}, X is on {dev}")
+    L = lib()
     with _on(dev):
-        dW = _result(out, (N, K), torch.bfloat16, dev)
-        L = lib()
-        nbytes = int(L.w4a16_gemm_wgrad_workspace_size(M, N))
+        dW = _result(out, (N, K), _BF16, dev)
+        nbytes = _scratch_bytes("w4a16_gemm_wgrad_workspace_size", dev, M, N)
         ws = _scratch(nbytes, dev)
-        _check(L.w4a16_gemm_wgrad(_p(dY), _p(X), M, N, K, _p(dW), _p(ws), nbytes,
-                                  torch.cuda.current_stream(dev).cuda_stream), "w4a16_gemm_wgrad")
+        _check(L.w4a16_gemm_wgrad(dY.data_ptr(), X.data_ptr(), M, N, K, dW.data_ptr(), _p(ws), nbytes,
+                                  _sid(dev)), "w4a16_gemm_wgrad")
     return dW
 
 
 def _need_ids(ids: torch.Tensor) -> int:
     if not isinstance(ids, torch.Tensor):
         raise TypeError("ids must be a torch.Tensor")
-    if ids.dtype not in (torch.int32, torch.int64):
+    if ids.dtype is not torch.int64 and ids.dtype is not torch.int32:
         raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
     if not ids.is_cuda:
         raise ValueError("ids must be on a CUDA device")
@@ -823,17 +855,17 @@ def _need_ids(ids: torch.Tensor) -> int:
 def _embedding(ids, w, g, sym, scale, out, bits):
     id_bytes = _need_ids(ids)
     sym = bool(sym)
-    codes, scales, zeros, V, K = _weights(w, None, sym, bits)
-    _groups_ok(scales, zeros, V, K, g)
+    codes, scales, zeros, V, K = _weights(w, None, g, sym, bits)
     dev = codes.device
-    _same_device(dev, ids=ids)
+    if ids.device != dev:
+        raise ValueError(f"ids is on {ids.device}, the table is on {dev}")
+    L = lib()
     with _on(dev):
-        Y = _result(out, (*ids.shape, K), torch.bfloat16, dev)
-        L = lib()
+        Y = _result(out, (*ids.shape, K), _BF16, dev)
         call = L.w8a16_embedding if bits == 8 else L.w4a16_embedding
-        _check(call(_p(ids), id_bytes, ids.numel(), _p(codes), _p(scales), _p(zeros), V, K, g, int(sym),
-                    float(scale), _p(Y), torch.cuda.current_stream(dev).cuda_stream),
-               f"w{bits}a16_embedding")
+        _check(call(ids.data_ptr(), id_bytes, ids.numel(), codes.data_ptr(), scales.data_ptr(), _p(zeros), V,
+                    K, g, sym, scale, Y.data_ptr(), _sid(dev)),
+               "w4a16_embedding" if bits == 4 else "w8a16_embedding")
     return Y
 
 
@@ -866,8 +898,8 @@ def embedding_grad(dY: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1
     id_bytes = _need_ids(ids)
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
-    _need(dY, torch.bfloat16, "dY", ndim=ids.dim() + 1)
-    if tuple(dY.shape[:-1]) != tuple(ids.shape):
+    _want(dY, _BF16, "dY", ids.dim() + 1)
+    if dY.shape[:-1] != ids.shape:
         raise ValueError(f"dY has shape {list(dY.shape)}, ids {list(ids.shape)}")
     dev = dY.device
     if ids.device != dev:
@@ -875,13 +907,12 @@ def embedding_grad(dY: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1
     V, K, T = int(V), dY.shape[-1], ids.numel()
     if V < 0:
         raise ValueError(f"V must not be negative, got {V}")
+    L = lib()
     with _on(dev):
         dW = _result(out, (V, K), dtype, dev)
-        L = lib()
-        nbytes = int(L.w4a16_embedding_grad_workspace_size(T, V, K))
+        nbytes = _scratch_bytes("w4a16_embedding_grad_workspace_size", dev, T, V, K)
         ws = _scratch(nbytes, dev)
-        _check(L.w4a16_embedding_grad(_p(dY), _p(ids), id_bytes, T, V, K, float(scale),
-                                      int(dtype == torch.float32), _p(dW), _p(ws), nbytes,
-                                      torch.cuda.current_stream(dev).cuda_stream),
+        _check(L.w4a16_embedding_grad(dY.data_ptr(), ids.data_ptr(), id_bytes, T, V, K, scale,
+                                      dtype is torch.float32, dW.data_ptr(), _p(ws), nbytes, _sid(dev)),
                "w4a16_embedding_grad")
     return dW

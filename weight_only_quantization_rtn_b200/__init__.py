@@ -649,9 +649,11 @@ def _weights(w, K: int | None, g: int, sym: bool, bits: int, name: str = ""):
     return codes, scales, zeros, N, kw
 
 
-def _result(out, shape: tuple, dtype: torch.dtype, dev, name: str = "out") -> torch.Tensor:
+def _result(out, shape: tuple, like: torch.Tensor, name: str = "out") -> torch.Tensor:
+    """``out`` checked, or a new tensor of ``like``'s type on its device."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return like.new_empty(shape)
+    dtype, dev = like.dtype, like.device
     _want(out, dtype, name, len(shape))
     if tuple(out.shape) != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(out.shape)}")
@@ -697,7 +699,7 @@ def _gated(X, gate, up, g, sym, act, out, save, path, static_weights, bits):
     pid = _PATHS[path] if isinstance(path, str) else int(path)
     L = lib()
     with _on(dev):
-        H = _result(out, (M, N), _BF16, dev)
+        H = _result(out, (M, N), gs)
         G = torch.empty_like(H) if save else None
         U = torch.empty_like(H) if save else None
         nbytes = _scratch_bytes("w8a16_gated_workspace_size" if bits == 8 else "w4a16_gated_workspace_size",
@@ -749,7 +751,7 @@ def _gated_backward(dH, G, U, gate, up, g, sym, act, out, bits):
     aid = _act_id(act)
     L = lib()
     with _on(dev):
-        dX = _result(out, (M, K), _BF16, dev)
+        dX = _result(out, (M, K), gs)
         dG, dU = torch.empty_like(dH), torch.empty_like(dH)
         nbytes = _scratch_bytes("w4a16_gated_backward_workspace_size", dev, M, N, K, g)
         ws = _scratch(nbytes, dev)
@@ -792,7 +794,7 @@ def _dgrad(dY, w, g, sym, out, bits):
         _same_device(dev, dY=dY)
     L = lib()
     with _on(dev):
-        dX = _result(out, (M, K), _BF16, dev)
+        dX = _result(out, (M, K), scales)
         nbytes = _scratch_bytes("w4a16_gemm_dgrad_workspace_size", dev, M, N, K, g)
         ws = _scratch(nbytes, dev)
         call = L.w8a16_gemm_dgrad if bits == 8 else L.w4a16_gemm_dgrad
@@ -832,7 +834,7 @@ def gemm_wgrad(dY: torch.Tensor, X: torch.Tensor, out: torch.Tensor | None = Non
         raise ValueError(f"dY is on {dY.device}, X is on {dev}")
     L = lib()
     with _on(dev):
-        dW = _result(out, (N, K), _BF16, dev)
+        dW = _result(out, (N, K), X)
         nbytes = _scratch_bytes("w4a16_gemm_wgrad_workspace_size", dev, M, N)
         ws = _scratch(nbytes, dev)
         _check(L.w4a16_gemm_wgrad(dY.data_ptr(), X.data_ptr(), M, N, K, dW.data_ptr(), _p(ws), nbytes,
@@ -861,7 +863,7 @@ def _embedding(ids, w, g, sym, scale, out, bits):
         raise ValueError(f"ids is on {ids.device}, the table is on {dev}")
     L = lib()
     with _on(dev):
-        Y = _result(out, (*ids.shape, K), _BF16, dev)
+        Y = _result(out, (*ids.shape, K), scales)
         call = L.w8a16_embedding if bits == 8 else L.w4a16_embedding
         _check(call(ids.data_ptr(), id_bytes, ids.numel(), codes.data_ptr(), scales.data_ptr(), _p(zeros), V,
                     K, g, sym, scale, Y.data_ptr(), _sid(dev)),
@@ -909,7 +911,14 @@ def embedding_grad(dY: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1
         raise ValueError(f"V must not be negative, got {V}")
     L = lib()
     with _on(dev):
-        dW = _result(out, (V, K), dtype, dev)
+        if out is None:
+            dW = torch.empty((V, K), dtype=dtype, device=dev)
+        else:
+            _want(out, dtype, "out")
+            if tuple(out.shape) != (V, K):
+                raise ValueError(f"out must have shape {[V, K]}, got {list(out.shape)}")
+            _same_device(dev, out=out)
+            dW = out
         nbytes = _scratch_bytes("w4a16_embedding_grad_workspace_size", dev, T, V, K)
         ws = _scratch(nbytes, dev)
         _check(L.w4a16_embedding_grad(dY.data_ptr(), ids.data_ptr(), id_bytes, T, V, K, scale,

@@ -251,7 +251,7 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parit
 // second, record the error and return false.  The global timer is read only once a
 // wait has lasted many tries: a read of it costs more than most waits of a pipeline.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (__builtin_expect(mbar_try_wait(bar, parity), true)) return true;
     uint64_t t0 = 0;
     for (uint32_t tries = 1;; ++tries) {
         if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;

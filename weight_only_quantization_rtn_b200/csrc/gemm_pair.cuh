@@ -366,6 +366,23 @@ __device__ __forceinline__ void sts128_addr(uint32_t addr, const uint32_t v[4]) 
                  : "memory");
 }
 
+// The same at a constant offset.
+template <int OFF>
+__device__ __forceinline__ void sts128_at(uint32_t addr, const uint32_t v[4]) {
+    asm volatile("st.shared.v4.u32 [%0 + %5], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "n"(OFF)
+                 : "memory");
+}
+
+template <int OFF>
+__device__ __forceinline__ uint4 lds128_at(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4 + %5];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr), "n"(OFF));
+    return v;
+}
+
 __device__ __forceinline__ uint4 lds128_addr(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -812,7 +829,13 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 // one warp of the group also vouches for the block's tokens
-                if (wg == 0) ok = mbar_wait(xfull + 8 * xslot, xph) && ok;
+                if (wg == 0) {
+                    ok = mbar_wait(xfull + 8 * xslot, xph) && ok;
+                    xslot += NG;
+                    const bool wrap = xslot >= SX;       // NG <= SX
+                    xslot -= wrap ? SX : 0;
+                    xph ^= wrap ? 1u : 0u;
+                }
                 if (lane == 0) {
                     if constexpr (PAIR) mbar_arrive_cluster(afull_r + 8 * ab);
                     else mbar_arrive(afull + 8 * ab);
@@ -820,12 +843,14 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                     // (a segment's last unit may have one block: its second arrival)
                     if (UB == 2 && i == nb - 1 && (i & 1) == 0) mbar_arrive(pempty + 8 * pslot);
                 }
-                xslot += NG;
-                while (xslot >= SX) { xslot -= SX; xph ^= 1u; }
                 ab += NG;
-                if (ab >= NA) { ab -= NA; aph ^= 1u; }
+                const bool awrap = ab >= NA;
+                ab -= awrap ? NA : 0;
+                aph ^= awrap ? 1u : 0u;
                 pslot += UB == 2 ? (NG == 2 ? 1 : 1 + (i & 1)) : NG;
-                while (pslot >= SP) { pslot -= SP; pph ^= 1u; }
+                const bool pwrap = pslot >= SP;          // a step is at most SP
+                pslot -= pwrap ? SP : 0;
+                pph ^= pwrap ? 1u : 0u;
             };
             if constexpr (!DGRAD) {
                 // thread = row r of both matrices
@@ -882,15 +907,22 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                                     for (int j = 0; j < 2; ++j) cur[t][j] = nxt[t][j];
                                 fetch(nxt, beyond(i));
                             }
+                            const uint32_t sel = vec && (ga & 1) ? 0x3232u : 0x1010u;
+                            const bool up = vec && (ga & 2) != 0;
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int g = h ? gb : ga;
-                                const uint32_t sel = vec && (g & 1) ? 0x3232u : 0x1010u;
-                                const bool up = vec ? (g & 2) != 0 : h == 1;
+                            for (int j = 0; j < 2; ++j) {
+                                sc[j][0] = sc[j][1] = __byte_perm(up ? cur[0][j].y : cur[0][j].x, 0u, sel);
+                                zc[j][0] = zc[j][1] =
+                                    pair_zero<BITS>(__byte_perm(up ? cur[1][j].y : cur[1][j].x, 0u, sel), sym, a.zsym);
+                            }
+                            if (gb != ga) {
+                                // (g = 32: ga is even, gb the other half of the same word)
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
-                                    sc[j][h] = __byte_perm(up ? cur[0][j].y : cur[0][j].x, 0u, sel);
-                                    zc[j][h] = pair_zero<BITS>(__byte_perm(up ? cur[1][j].y : cur[1][j].x, 0u, sel), sym, a.zsym);
+                                    const uint32_t sw = vec ? (up ? cur[0][j].y : cur[0][j].x) >> 16 : cur[0][j].y;
+                                    const uint32_t zw = vec ? (up ? cur[1][j].y : cur[1][j].x) >> 16 : cur[1][j].y;
+                                    sc[j][1] = dup16(sw);
+                                    zc[j][1] = pair_zero<BITS>(dup16(zw), sym, a.zsym);
                                 }
                             }
                             have = ga;
@@ -901,12 +933,12 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                         ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
                         if (!ok) break;
                         uint4 v[2][BITS / 2];
+                        const uint32_t prow = (lds0 + (uint32_t)(pslot * Unit::kBytes)) ^ (UB == 2 ? 32u * (i & 1) : 0u);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-#pragma unroll
-                            for (int c = 0; c < BITS / 2; ++c)
-                                v[j][c] = lds128_addr((lds0 + (uint32_t)(pslot * Unit::kBytes + j * (Unit::kBytes / 2))) ^
-                                                      (uint32_t)(16 * c + (UB == 2 ? 32 * (i & 1) : 0)));
+                        for (int c = 0; c < BITS / 2; ++c) {
+                            v[0][c] = lds128_at<0>(prow ^ (uint32_t)(16 * c));
+                            v[1][c] = lds128_at<Unit::kBytes / 2>(prow ^ (uint32_t)(16 * c));
+                        }
                         const uint32_t arow = as + (uint32_t)(ab * kPairABytes) + sts0;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -922,7 +954,8 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                                     pair_dequant8<8>((c & 1) ? q.z : q.x, (c & 1) ? q.w : q.y, a.flip, zc[j][c >> 2],
                                                      sc[j][c >> 2], d);
                                 }
-                                sts128_addr((arow ^ (uint32_t)(16 * c)) + (uint32_t)(j * (kPairABytes / 2)), d);
+                                if (j == 0) sts128_at<0>(arow ^ (uint32_t)(16 * c), d);
+                                else sts128_at<kPairABytes / 2>(arow ^ (uint32_t)(16 * c), d);
                             }
                         }
                         release();
@@ -1009,7 +1042,8 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                                     const uint32_t w1 = (c & 1) ? (q ? x1.w : x0.w) : (q ? x1.y : x0.y);
                                     pair_dequant8<8>(w0, w1, a.flip, zz, ss, d);
                                 }
-                                sts128_addr((aline ^ (uint32_t)(16 * c)) + (uint32_t)(b * 8192), d);
+                                if (b == 0) sts128_at<0>(aline ^ (uint32_t)(16 * c), d);
+                                else sts128_at<8192>(aline ^ (uint32_t)(16 * c), d);
                             }
                         }
                         release();

@@ -138,6 +138,38 @@ __device__ __forceinline__ void tc_mma_bf16_g(uint32_t tmem_d, uint64_t adesc, u
         tc_mma_bf16(tmem_d, adesc, bdesc, idesc, accumulate);
 }
 
+// D += A·B with A (128 rows x 16 of the reduction, 8 columns) in tensor memory.
+__device__ __forceinline__ void tc_mma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// This thread's 32 columns of its lane of tensor memory.
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]), "r"(r[1]),
+        "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+
 // Arrive on the barrier at `bar` (PAIR: on the same barrier of both CTAs) once all MMAs
 // issued so far have completed.
 template <bool PAIR>
@@ -188,39 +220,60 @@ constexpr int kPairMaxX = 8;
 constexpr int kPairMaxWarps = 12;       // dequantizing warps, at most
 
 // A pair's MMAs take longer than two groups of dequantizing warps need for a block; a single
-// CTA's small tiles do not, so it has a third group and a fourth A buffer for it, and smaller
-// rings of loads (M = 61, K = 8192, N = 18944: 84.7 us with two groups, 79.6 us with three;
-// the gradient with M = 77, K = 37888, N = 8192: 157 and 133 us).  With 8-bit codes, whose
-// units are larger, a third group gained nothing (102 us both).
-template <bool PAIR, int BITS>
+// CTA's small tiles do not, so with 4-bit codes it has a third group (the gradient with
+// M = 77, K = 37888, N = 8192: 157 us with two groups, 133 us with three; 8-bit codes: no gain).
+//
+// kTmemA: a single CTA's GATED tiles leave tensor memory free, and what paced them with the A
+// tiles in shared memory was its bandwidth (0.57 us per block at any token count, 0.39 us
+// without the stores).  So there the dequantized weights go to tensor memory (a lane is a
+// weight row, K-major as the MMA reads A from there) and never touch shared memory, which
+// holds deep rings of loads instead.  DGRAD cannot: its A is the transpose of what a thread has.
+constexpr int kPairMaxA = 6;
+template <bool PAIR, int BITS, bool DGRAD>
 struct PairConfig {
+    static constexpr bool kTmemA = !PAIR && !DGRAD;
     static constexpr int kGroups = !PAIR && BITS == 4 ? 3 : 2;
     static constexpr int kWarps = 4 * kGroups;                 // warps 4 .. 4 + kWarps - 1
     static constexpr int kThreads = (4 + kWarps) * 32;
-    static constexpr int kABufs = kGroups + 1;
+    static constexpr int kSmemA = kTmemA ? 0 : (kGroups + 1) * kPairABytes;   // A ring
     static constexpr int kStage = kWarps * 1024;               // epilogue staging, 1 KB per warp
-    static constexpr int kLoads = kGroups == 2 ? 112 * 1024 : 84 * 1024;   // token and code rings
-    static constexpr int kSmem = kABufs * kPairABytes + kStage + kLoads + 1024 + 1024;
+    static constexpr int kLoads = kTmemA ? 225 * 1024 - kStage : (kGroups == 2 ? 112 * 1024 : 84 * 1024);
+    static constexpr int kSmem = kSmemA + kStage + kLoads + 1024 + 1024;
     static_assert(kSmem <= 232448, "shared memory");
+    // 64-wide blocks per code unit, and its bytes: two boxes (gate, up) of 128 rows, of 128 bytes
+    // with kTmemA and 64 bytes in a pair's tighter ring; DGRAD: 64 rows x 256 channels.
+    static constexpr int kUnitBlocks = DGRAD ? 1 : (kTmemA ? 2 : 1) * 8 / BITS;
+    static constexpr int kUnitBytes = 2 * kPairRows * kPairBlock * BITS / 8 * kUnitBlocks;
 };
 
 // Most tokens of a tile of one CTA: its token ring must hold a block for each A buffer.
 constexpr int kPairMaxSingle = 96;
 
-// Bytes of the code ring; the token ring has the rest of the loads' space.  Both rings hold
-// at least kABufs blocks, so that a free A slot implies that what their slots held before was
-// used: a warp that awaits a slot's next phase cannot be looking at an older one.
-template <int GROUPS>
-__host__ __device__ constexpr int pair_code_ring(int bt) {
-    return GROUPS == 2 || bt <= 64 ? 48 * 1024 : 32 * 1024;
-}
-
-// Blocks of 64 that one code unit covers, and its bytes.
-template <int BITS, bool DGRAD>
-struct PairUnit {
-    static constexpr int kBlocks = (!DGRAD && BITS == 4) ? 2 : 1;
-    static constexpr int kBytes = 2 * kPairRows * kPairBlock * BITS / 8 * kBlocks;
+// A slots, code units and token blocks that the rings hold.  The latter two cover at least as
+// many blocks as there are A slots, so that a free A slot implies that what their slots held
+// before was used: a warp that awaits a slot's next phase cannot be looking at an older one.
+struct PairRings {
+    int na, sp, sx;
 };
+template <typename Cfg>
+__host__ __device__ inline PairRings pair_rings(int bt, int acc_cols) {
+    const int x_bytes = bt * kPairBlock * 2;
+    PairRings r;
+    if (Cfg::kTmemA) {
+        r.na = (512 - 2 * acc_cols) / 64;
+        if (r.na > kPairMaxA) r.na = kPairMaxA;
+        r.sx = (Cfg::kLoads - 4 * Cfg::kUnitBytes) / x_bytes;
+        if (r.sx > kPairMaxX) r.sx = kPairMaxX;
+        r.sp = (Cfg::kLoads - r.sx * x_bytes) / Cfg::kUnitBytes;
+    } else {
+        r.na = Cfg::kGroups + 1;
+        r.sp = (Cfg::kGroups == 2 || bt <= 64 ? 48 * 1024 : 32 * 1024) / Cfg::kUnitBytes;
+        r.sx = (Cfg::kLoads - r.sp * Cfg::kUnitBytes) / x_bytes;
+        if (r.sx > kPairMaxX) r.sx = kPairMaxX;
+    }
+    if (r.sp > kPairMaxX) r.sp = kPairMaxX;
+    return r;
+}
 
 struct PairArgs {
     const uint16_t* scales[2];   // GATED: gate, up; DGRAD: one per product
@@ -598,29 +651,27 @@ __device__ __forceinline__ bool pair_epilogue(const PairArgs& a, const PairTileD
 }
 
 template <bool PAIR, int BITS, bool DGRAD>
-__global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
+__global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
     gemm_pair_kernel(const __grid_constant__ CUtensorMap tmX0, const __grid_constant__ CUtensorMap tmX1,
                      const __grid_constant__ CUtensorMap tmP0, const __grid_constant__ CUtensorMap tmP1,
                      const __grid_constant__ PairArgs a) {
-    using Unit = PairUnit<BITS, DGRAD>;
-    using Cfg = PairConfig<PAIR, BITS>;
-    constexpr int UB = Unit::kBlocks, NA = Cfg::kABufs, NG = Cfg::kGroups;
+    using Cfg = PairConfig<PAIR, BITS, DGRAD>;
+    constexpr int UB = Cfg::kUnitBlocks, NG = Cfg::kGroups;
     constexpr int kCtas = PAIR ? 2 : 1;
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const int p_ring = pair_code_ring<NG>(a.bt), x_bytes = a.bt * kPairBlock * 2;
-    const int SP = min(p_ring / Unit::kBytes, kPairMaxX);             // code units
-    const int SX = min((Cfg::kLoads - p_ring) / x_bytes, kPairMaxX);  // token blocks
-    const uint32_t as = smem_u32(smem);              // NA x kPairABytes
-    const uint32_t ps = as + NA * kPairABytes;       // code ring
-    const uint32_t xs = ps + p_ring;                 // token ring
+    const PairRings rings = pair_rings<Cfg>(a.bt, a.acc_cols);
+    const int NA = rings.na, SP = rings.sp, SX = rings.sx, x_bytes = a.bt * kPairBlock * 2;
+    const uint32_t as = smem_u32(smem);              // NA x kPairABytes (not with kTmemA)
+    const uint32_t ps = as + Cfg::kSmemA;            // SP code units
+    const uint32_t xs = ps + SP * Cfg::kUnitBytes;   // SX token blocks
     const uint32_t st = ps + Cfg::kLoads;            // epilogue staging
     const uint32_t bars = st + Cfg::kStage;
     const uint32_t xfull = bars, xempty = xfull + 8 * kPairMaxX;
     const uint32_t pfull = xempty + 8 * kPairMaxX, pempty = pfull + 8 * kPairMaxX;
-    const uint32_t afull = pempty + 8 * kPairMaxX, aempty = afull + 8 * NA;
-    const uint32_t accf = aempty + 8 * NA, accempty = accf + 8;
+    const uint32_t afull = pempty + 8 * kPairMaxX, aempty = afull + 8 * kPairMaxA;
+    const uint32_t accf = aempty + 8 * kPairMaxA, accempty = accf + 8;
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + (accempty + 8 - as));
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
@@ -655,13 +706,15 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
         prefetch_tensormap(&tmP0);
         if (!DGRAD || a.products > 1) prefetch_tensormap(&tmP1);
     }
-    if (warp == 1) tmem_alloc_g<PAIR>(smem_u32(tmem_holder), 2 * a.acc_cols);
+    const int tmem_cols = Cfg::kTmemA ? 512 : 2 * a.acc_cols;
+    if (warp == 1) tmem_alloc_g<PAIR>(smem_u32(tmem_holder), tmem_cols);
     tc_fence_before();
     __syncwarp();
     __syncthreads();
     if constexpr (PAIR) cluster_sync_all();      // the pair's barriers are set up before either arrives
     tc_fence_after();
     const uint32_t tmem_d = *tmem_holder;
+    const uint32_t tmem_a = tmem_d + (uint32_t)(512 - 64 * NA);      // kTmemA: NA x (gate 32, up 32 columns)
     PairWalk<UB> walk;
     walk.init(a, slot, slots);
 
@@ -705,8 +758,8 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                 for (int u = 0; u < walk.units; ++u) {
                     ok = mbar_wait(pempty + 8 * s, ph ^ 1u);
                     if (!ok) break;
-                    const uint32_t bar = pfull + 8 * s, p = ps + s * Unit::kBytes;
-                    mbar_arrive_expect_tx(bar, Unit::kBytes);
+                    const uint32_t bar = pfull + 8 * s, p = ps + s * Cfg::kUnitBytes;
+                    mbar_arrive_expect_tx(bar, Cfg::kUnitBytes);
                     if constexpr (DGRAD) {
                         int b = walk.u0 + u;
                         const CUtensorMap* tp = &tmP0;
@@ -721,7 +774,7 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                     } else {
                         const int k = (walk.u0 + u) * UB * kPairBlock, n = r0 + rank * kPairRows;
                         tma_load_2d(p, &tmP0, k * BITS / 8, n, bar);
-                        tma_load_2d(p + Unit::kBytes / 2, &tmP1, k * BITS / 8, n, bar);
+                        tma_load_2d(p + Cfg::kUnitBytes / 2, &tmP1, k * BITS / 8, n, bar);
                     }
                     ++issued;
                     if (++s == SP) { s = 0; ph ^= 1u; }
@@ -761,8 +814,14 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < kPairBlock / 16; ++kk) {
                             const uint32_t acc = (i | kk) != 0 ? 1u : 0u;
-                            tc_mma_bf16_g<PAIR>(tmem_d, ad + kk * kStepA, bd + kk * 2, idesc, acc);
-                            tc_mma_bf16_g<PAIR>(acc1, ad + (kPairABytes / 32 + kk * kStepA), bd + kk * 2, idesc, acc);
+                            if constexpr (Cfg::kTmemA) {
+                                const uint32_t at = tmem_a + (uint32_t)(64 * ab + 8 * kk);
+                                tc_mma_bf16_ta(tmem_d, at, bd + kk * 2, idesc, acc);
+                                tc_mma_bf16_ta(acc1, at + 32, bd + kk * 2, idesc, acc);
+                            } else {
+                                tc_mma_bf16_g<PAIR>(tmem_d, ad + kk * kStepA, bd + kk * 2, idesc, acc);
+                                tc_mma_bf16_g<PAIR>(acc1, ad + (kPairABytes / 32 + kk * kStepA), bd + kk * 2, idesc, acc);
+                            }
                         }
                         tc_commit_g<PAIR>(xempty + 8 * s);
                         tc_commit_g<PAIR>(aempty + 8 * ab);
@@ -826,7 +885,12 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
             // loads, a slot was seen refilled before a load of it had been performed.)
             int i = grp;
             auto release = [&]() {
-                fence_proxy_async_smem();
+                if constexpr (Cfg::kTmemA) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                } else {
+                    fence_proxy_async_smem();
+                }
                 __syncwarp();
                 // one warp of the group also vouches for the block's tokens
                 if (wg == 0) {
@@ -839,15 +903,15 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                 if (lane == 0) {
                     if constexpr (PAIR) mbar_arrive_cluster(afull_r + 8 * ab);
                     else mbar_arrive(afull + 8 * ab);
-                    mbar_arrive(pempty + 8 * pslot);
-                    // (a segment's last unit may have one block: its second arrival)
-                    if (UB == 2 && i == nb - 1 && (i & 1) == 0) mbar_arrive(pempty + 8 * pslot);
+                    // (a segment's last unit may have fewer blocks: the last one arrives for them too)
+                    if (UB > 1 && i == nb - 1) mbar_arrive_n(pempty + 8 * pslot, (uint32_t)(UB - i % UB));
+                    else mbar_arrive(pempty + 8 * pslot);
                 }
                 ab += NG;
                 const bool awrap = ab >= NA;
                 ab -= awrap ? NA : 0;
                 aph ^= awrap ? 1u : 0u;
-                pslot += UB == 2 ? (NG == 2 ? 1 : 1 + (i & 1)) : NG;
+                pslot += (i % UB + NG) / UB;
                 const bool pwrap = pslot >= SP;          // a step is at most SP
                 pslot -= pwrap ? SP : 0;
                 pph ^= pwrap ? 1u : 0u;
@@ -860,7 +924,9 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                 const bool vec = (a.groups & 3) == 0;         // rows of scales are 8-byte aligned
                 const int64_t srow = (int64_t)n * a.groups;
                 const uint32_t sts0 = (uint32_t)(r * 128 + ((r & 7) * 16));               // chunk c: ^ 16·c
-                const uint32_t lds0 = ps + (uint32_t)(r * 64 + ((r >> 1) & 3) * 16);      // chunk c: ^ 16·c
+                // this row's codes in a unit; logical chunk c is at ^ 16·c (128- or 64-byte swizzle)
+                const uint32_t lds0 = ps + (Cfg::kTmemA ? (uint32_t)(r * 128 + (r & 7) * 16)
+                                                        : (uint32_t)(r * 64 + ((r >> 1) & 3) * 16));
                 auto group_of = [&](int blk, int h) {
                     return min(((b0 + blk) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
                 };
@@ -933,15 +999,17 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                         ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
                         if (!ok) break;
                         uint4 v[2][BITS / 2];
-                        const uint32_t prow = (lds0 + (uint32_t)(pslot * Unit::kBytes)) ^ (UB == 2 ? 32u * (i & 1) : 0u);
+                        const uint32_t prow = (lds0 + (uint32_t)(pslot * Cfg::kUnitBytes)) ^ (uint32_t)(8 * BITS * (i % UB));
 #pragma unroll
                         for (int c = 0; c < BITS / 2; ++c) {
                             v[0][c] = lds128_at<0>(prow ^ (uint32_t)(16 * c));
-                            v[1][c] = lds128_at<Unit::kBytes / 2>(prow ^ (uint32_t)(16 * c));
+                            v[1][c] = lds128_at<Cfg::kUnitBytes / 2>(prow ^ (uint32_t)(16 * c));
                         }
                         const uint32_t arow = as + (uint32_t)(ab * kPairABytes) + sts0;
+                        if constexpr (Cfg::kTmemA) tc_fence_after();          // behind the MMAs that read the slot
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
+                            uint32_t o[32];                     // kTmemA: the row's 64 weights
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
                                 uint32_t d[4];
@@ -954,9 +1022,17 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                                     pair_dequant8<8>((c & 1) ? q.z : q.x, (c & 1) ? q.w : q.y, a.flip, zc[j][c >> 2],
                                                      sc[j][c >> 2], d);
                                 }
-                                if (j == 0) sts128_at<0>(arow ^ (uint32_t)(16 * c), d);
-                                else sts128_at<kPairABytes / 2>(arow ^ (uint32_t)(16 * c), d);
+                                if constexpr (Cfg::kTmemA) {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[4 * c + e] = d[e];
+                                } else if (j == 0) {
+                                    sts128_at<0>(arow ^ (uint32_t)(16 * c), d);
+                                } else {
+                                    sts128_at<kPairABytes / 2>(arow ^ (uint32_t)(16 * c), d);
+                                }
                             }
+                            if constexpr (Cfg::kTmemA)
+                                tmem_st_32x32b_x32(tmem_a + (uint32_t)(64 * ab + 32 * j) + ((uint32_t)(wg * 32) << 16), o);
                         }
                         release();
                     }
@@ -1017,7 +1093,7 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
                         ok = mbar_wait(aempty + 8 * ab, aph ^ 1u) && ok;       // first, as above
                         ok = mbar_wait(pfull + 8 * pslot, pph) && ok;
                         if (!ok) break;
-                        const uint32_t prow = row + (uint32_t)(pslot * Unit::kBytes);
+                        const uint32_t prow = row + (uint32_t)(pslot * Cfg::kUnitBytes);
                         uint4 v[BITS];                           // the thread's codes
 #pragma unroll
                         for (int c = 0; c < BITS; ++c)
@@ -1068,7 +1144,7 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS>::kThreads, 1)
     if constexpr (PAIR) cluster_sync_all();      // neither CTA leaves while the other may still use it
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_g<PAIR>(tmem_d, 2 * a.acc_cols);
+        tmem_dealloc_g<PAIR>(tmem_d, tmem_cols);
     }
 }
 

@@ -141,7 +141,7 @@ w4a16_status launch_pair_t(const PairPlan& p, const CUtensorMap* tmX, const CUte
                            void* workspace, cudaStream_t stream) {
     auto kern = gemm_pair_kernel<PAIR, BITS, DGRAD>;
     static bool done[kMaxDevices] = {};
-    w4a16_status st = set_smem(kern, PairConfig<PAIR, BITS>::kSmem, done);
+    w4a16_status st = set_smem(kern, PairConfig<PAIR, BITS, DGRAD>::kSmem, done);
     if (st != W4A16_OK) return st;
     args.bt = p.bt;
     args.acc_cols = 32;
@@ -161,8 +161,8 @@ w4a16_status launch_pair_t(const PairPlan& p, const CUtensorMap* tmX, const CUte
     attr[0].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.grid * p.ctas), 1, 1);
-    cfg.blockDim = dim3(PairConfig<PAIR, BITS>::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = PairConfig<PAIR, BITS>::kSmem;
+    cfg.blockDim = dim3(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = PairConfig<PAIR, BITS, DGRAD>::kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 1 : 0;
@@ -272,6 +272,13 @@ w4a16_status launch_gated_decode_g(int gsel, int64_t grid, int smem, const Decod
 }
 
 // What a gated call runs: the decode kernel for at most 16 tokens, else the tensor cores.
+// 64-wide blocks per code unit of the tensor-core kernel (PairConfig::kUnitBlocks).
+int gated_unit_blocks(int64_t M, int bits) {
+    if (M > kPairMaxSingle)
+        return bits == 8 ? PairConfig<true, 8, false>::kUnitBlocks : PairConfig<true, 4, false>::kUnitBlocks;
+    return bits == 8 ? PairConfig<false, 8, false>::kUnitBlocks : PairConfig<false, 4, false>::kUnitBlocks;
+}
+
 struct GatedPlan {
     bool decode;
     DecodeGeometry d;
@@ -294,7 +301,7 @@ w4a16_status gated_plan(int64_t M, int64_t N, int64_t K, int32_t g, int32_t path
         if (q.grid < 1) q.grid = 1;
         q.bytes = decode_workspace_bytes(q.d, q.grid);
     } else {
-        q.p = pair_plan(M, N, kPairRows, (K + kPairBlock - 1) / kPairBlock, bits == 4 ? 2 : 1, current_sm_count());
+        q.p = pair_plan(M, N, kPairRows, (K + kPairBlock - 1) / kPairBlock, gated_unit_blocks(M, bits), current_sm_count());
         q.bytes = q.p.bytes;
     }
     *out = q;
@@ -395,7 +402,8 @@ w4a16_status gated_impl(const void* X, int64_t M, int64_t K, const Weights* w, i
     const uint64_t row_bytes = (uint64_t)K * bits / 8;
     for (int i = 0; i < 2; ++i) {
         st = encode_rows(&tmP[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w[i].codes, row_bytes, (uint64_t)N, row_bytes,
-                         64, kPairRows, CU_TENSOR_MAP_SWIZZLE_64B);
+                         q.p.ctas == 2 ? 64 : 128, kPairRows,
+                         q.p.ctas == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
         if (st != W4A16_OK) return st;
     }
     PairArgs a{};

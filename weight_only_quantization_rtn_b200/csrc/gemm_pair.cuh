@@ -373,30 +373,47 @@ __device__ __forceinline__ bool pair_wait_flag(const uint64_t* flag) {
     }
 }
 
-// Zero point as the dequantization wants it, from the bf16 pair (z, z): the pair of
-// 128 + z (4-bit codes), or the binary32 2^23 + z (8-bit codes).
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// A scale and zero point as the dequantization wants them, from bf16 pairs (s, s), (z, z).
+// 4-bit codes: s·2^6 and −z·2^-6 (see below; exact while s < 2^122); 8-bit codes: s and the
+// binary32 2^23 + z.
+template <int BITS>
+__device__ __forceinline__ uint32_t pair_scale(uint32_t ss) {
+    return BITS == 4 ? bf16x2_mul(ss, 0x42804280u) : ss;
+}
+
 template <int BITS>
 __device__ __forceinline__ uint32_t pair_zero(uint32_t zz, bool sym, float zsym) {
-    if (BITS == 4) return sym ? 0x43084308u : bf16x2_add(zz, 0x43004300u);
+    if (BITS == 4) return sym ? 0xBE00BE00u : bf16x2_mul(zz, 0xBC80BC80u);       // −8·2^-6; −2^-6·z
     return __float_as_uint(8388608.0f + (sym ? zsym : __uint_as_float(zz & 0xFFFF0000u)));
 }
 
-// Eight codes -> four bf16 pairs in natural order.  4 bits (w0): PRMT brings code 2j of
-// the word and code 2j + 1 of the word shifted by 4 into the low bytes of the halves, one
-// LOP3 masks the nibbles and sets the exponent of 128 (symmetric codes: bit 3 flipped in
-// the same LOP3).  8 bits (w0, w1): as dequant4_bytes in gemm_tcgen05.cuh.
+// Eight codes -> four bf16 pairs in natural order.
+// 4 bits (w0): the nibbles are split into two words of bytes (symmetric codes: bit 3 flipped
+// in the same LOP3), PRMT puts code 2j and code 2j + 1 into the halves of a word with zero
+// bytes above: as bf16 a half is the subnormal q·2^-133.  One fma with 2^127 and −z·2^-6
+// gives (q − z)·2^-6 exactly, one multiplication by s·2^6 rounds (q − z)·s once.  15
+// instructions, seven of them on the half-rate integer pipe, which paces the kernel at
+// small token counts (with the exponent set by a LOP3 and a subtraction: 17 and nine).
+// 8 bits (w0, w1): as dequant4_bytes in gemm_tcgen05.cuh.
 template <int BITS>
 __device__ __forceinline__ void pair_dequant8(uint32_t w0, uint32_t w1, uint32_t flip, uint32_t zz,
                                               uint32_t ss, uint32_t out[4]) {
     if constexpr (BITS == 4) {
-        const uint32_t magic = 0x43004300u | (flip & 0x00080008u), hi = w0 >> 4;
+        const uint32_t lo = (w0 ^ flip) & 0x0F0F0F0Fu, hi = ((w0 >> 4) ^ flip) & 0x0F0F0F0Fu;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            // bytes: [w.j, any, (w >> 4).j, any]
-            const uint32_t sel = (uint32_t)j | ((uint32_t)j << 4) | ((uint32_t)(4 + j) << 8) | ((uint32_t)(4 + j) << 12);
+            // bytes [lo.j, 0, hi.j, 0]: selector 8 | x replicates the (zero) sign bit, which the
+            // PTX instruction does and __byte_perm does not
+            const uint32_t sel = (uint32_t)j | 0x80u | ((uint32_t)(4 + j) << 8) | 0xC000u;
             uint32_t q;
-            asm("lop3.b32 %0, %1, 0x000F000F, %2, 0x6A;" : "=r"(q) : "r"(__byte_perm(w0, hi, sel)), "r"(magic));
-            out[j] = bf16x2_mul(bf16x2_sub(q, zz), ss);
+            asm("prmt.b32 %0, %1, %2, %3;" : "=r"(q) : "r"(lo), "r"(hi), "r"(sel));
+            out[j] = bf16x2_mul(bf16x2_fma(q, 0x7F007F00u, zz), ss);
         }
     } else {
         const float s = __uint_as_float(ss & 0xFFFF0000u), zoff = __uint_as_float(zz);
@@ -728,7 +745,7 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
                 const int b0 = walk.first_block(), nb = walk.count(a);
                 const int m0 = walk.tile % a.tiles_m * mma_n + rank * a.bt;
                 for (int i = 0; i < nb; ++i) {
-                    ok = mbar_wait(xempty + 8 * s, ph ^ 1u);
+                    ok = mbar_wait_backoff(xempty + 8 * s, ph ^ 1u, 128u);
                     if (!ok) break;
                     mbar_arrive_expect_tx(xfull + 8 * s, x_bytes);
                     int b = b0 + i;
@@ -756,7 +773,7 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
             while (ok && walk.next(a, slots)) {
                 const int r0 = pair_row0<DGRAD>(a, walk.tile, kCtas);
                 for (int u = 0; u < walk.units; ++u) {
-                    ok = mbar_wait(pempty + 8 * s, ph ^ 1u);
+                    ok = mbar_wait_backoff(pempty + 8 * s, ph ^ 1u, 128u);
                     if (!ok) break;
                     const uint32_t bar = pfull + 8 * s, p = ps + s * Cfg::kUnitBytes;
                     mbar_arrive_expect_tx(bar, Cfg::kUnitBytes);
@@ -977,7 +994,7 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
                             const bool up = vec && (ga & 2) != 0;
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                sc[j][0] = sc[j][1] = __byte_perm(up ? cur[0][j].y : cur[0][j].x, 0u, sel);
+                                sc[j][0] = sc[j][1] = pair_scale<BITS>(__byte_perm(up ? cur[0][j].y : cur[0][j].x, 0u, sel));
                                 zc[j][0] = zc[j][1] =
                                     pair_zero<BITS>(__byte_perm(up ? cur[1][j].y : cur[1][j].x, 0u, sel), sym, a.zsym);
                             }
@@ -987,7 +1004,7 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
                                 for (int j = 0; j < 2; ++j) {
                                     const uint32_t sw = vec ? (up ? cur[0][j].y : cur[0][j].x) >> 16 : cur[0][j].y;
                                     const uint32_t zw = vec ? (up ? cur[1][j].y : cur[1][j].x) >> 16 : cur[1][j].y;
-                                    sc[j][1] = dup16(sw);
+                                    sc[j][1] = pair_scale<BITS>(dup16(sw));
                                     zc[j][1] = pair_zero<BITS>(dup16(zw), sym, a.zsym);
                                 }
                             }
@@ -1081,7 +1098,7 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
                         for (int t = 0; t < 4; ++t) {
                             const uint32_t sv = pieces == 4 ? sa[t] : (pieces == 2 ? sa[t >> 1] : sa[0]);
                             const uint32_t zv = pieces == 4 ? za[t] : (pieces == 2 ? za[t >> 1] : za[0]);
-                            sc[t] = dup16(sv);
+                            sc[t] = pair_scale<BITS>(dup16(sv));
                             zc[t] = pair_zero<BITS>(dup16(zv), sym, a.zsym);
                         }
 #pragma unroll

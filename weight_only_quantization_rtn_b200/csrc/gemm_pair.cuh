@@ -220,8 +220,9 @@ constexpr int kPairMaxX = 8;
 constexpr int kPairMaxWarps = 12;       // dequantizing warps, at most
 
 // A pair's MMAs take longer than two groups of dequantizing warps need for a block; a single
-// CTA's small tiles do not, so with 4-bit codes it has a third group (the gradient with
-// M = 77, K = 37888, N = 8192: 157 us with two groups, 133 us with three; 8-bit codes: no gain).
+// CTA's small tiles do not, so its 4-bit gradient has a third group (M = 77, K = 37888,
+// N = 8192: 157 us with two groups, 133 us with three).  Three gained nothing with 8-bit codes
+// and spilled in the gated form (M = 61, K = 4096, N = 11008: 37.8 us with two, 40.3 with three).
 //
 // kTmemA: a single CTA's GATED tiles leave tensor memory free, and what paced them with the A
 // tiles in shared memory was its bandwidth (0.57 us per block at any token count, 0.39 us
@@ -232,7 +233,7 @@ constexpr int kPairMaxA = 6;
 template <bool PAIR, int BITS, bool DGRAD>
 struct PairConfig {
     static constexpr bool kTmemA = !PAIR && !DGRAD;
-    static constexpr int kGroups = !PAIR && BITS == 4 ? 3 : 2;
+    static constexpr int kGroups = !PAIR && DGRAD && BITS == 4 ? 3 : 2;
     static constexpr int kWarps = 4 * kGroups;                 // warps 4 .. 4 + kWarps - 1
     static constexpr int kThreads = (4 + kWarps) * 32;
     static constexpr int kSmemA = kTmemA ? 0 : (kGroups + 1) * kPairABytes;   // A ring
@@ -286,7 +287,6 @@ struct PairArgs {
     int gshift;                  // log2 g; 31 for per-channel (one group per row)
     int groups;                  // groups per row
     uint32_t flip;               // symmetric codes: 0x88888888 or 0x80808080, else 0
-    float zsym;                  // symmetric codes: 8 or 128 (the flipped code of 0), else 0
     int act;
     int products;                // DGRAD: 1 or 2
     int bt;                      // tokens of a CTA's tile (PAIR: half of the tile's)
@@ -379,54 +379,48 @@ __device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t 
     return d;
 }
 
-// A scale and zero point as the dequantization wants them, from bf16 pairs (s, s), (z, z).
-// 4-bit codes: s·2^6 and −z·2^-6 (see below; exact while s < 2^122); 8-bit codes: s and the
-// binary32 2^23 + z.
-template <int BITS>
-__device__ __forceinline__ uint32_t pair_scale(uint32_t ss) {
-    return BITS == 4 ? bf16x2_mul(ss, 0x42804280u) : ss;
-}
+// A scale and zero point as the dequantization wants them, from bf16 pairs (s, s), (z, z):
+// s·2^6 and −z·2^-6 (see below; exact while s < 2^122).  Symmetric codes are flipped to
+// offset form and take z = 8 or 128.
+__device__ __forceinline__ uint32_t pair_scale(uint32_t ss) { return bf16x2_mul(ss, 0x42804280u); }
 
 template <int BITS>
-__device__ __forceinline__ uint32_t pair_zero(uint32_t zz, bool sym, float zsym) {
-    if (BITS == 4) return sym ? 0xBE00BE00u : bf16x2_mul(zz, 0xBC80BC80u);       // −8·2^-6; −2^-6·z
-    return __float_as_uint(8388608.0f + (sym ? zsym : __uint_as_float(zz & 0xFFFF0000u)));
+__device__ __forceinline__ uint32_t pair_zero(uint32_t zz, bool sym) {
+    constexpr uint32_t kSym = BITS == 4 ? 0xBE00BE00u : 0xC000C000u;             // −8·2^-6, −128·2^-6
+    return sym ? kSym : bf16x2_mul(zz, 0xBC80BC80u);
 }
 
 // Eight codes -> four bf16 pairs in natural order.
-// 4 bits (w0): the nibbles are split into two words of bytes (symmetric codes: bit 3 flipped
-// in the same LOP3), PRMT puts code 2j and code 2j + 1 into the halves of a word with zero
-// bytes above: as bf16 a half is the subnormal q·2^-133.  One fma with 2^127 and −z·2^-6
-// gives (q − z)·2^-6 exactly, one multiplication by s·2^6 rounds (q − z)·s once.  15
-// instructions, seven of them on the half-rate integer pipe, which paces the kernel at
-// small token counts (with the exponent set by a LOP3 and a subtraction: 17 and nine).
-// 8 bits (w0, w1): as dequant4_bytes in gemm_tcgen05.cuh.
+// A code q of 4 or 8 bits alone in a 16-bit half is, as bf16, q·2^-133 exactly (subnormal, or
+// in the first normal binade, which continues the same steps).  One fma with 2^127 and
+// −z·2^-6 gives (q − z)·2^-6 exactly (an integer of at most 8 bits), one multiplication by
+// s·2^6 rounds (q − z)·s once.  PRMT brings the codes into the halves: 4 bits (w0) from
+// two words of nibbles split into bytes, 8 bits (w0, w1) from the bytes themselves.  15 (4
+// bits) and 14 (8 bits) instructions; with the exponent set by a LOP3 and a subtraction 17,
+// and with 8-bit codes formed in binary32 30, which paced the kernel.
 template <int BITS>
 __device__ __forceinline__ void pair_dequant8(uint32_t w0, uint32_t w1, uint32_t flip, uint32_t zz,
                                               uint32_t ss, uint32_t out[4]) {
+    uint32_t lo, hi;
     if constexpr (BITS == 4) {
-        const uint32_t lo = (w0 ^ flip) & 0x0F0F0F0Fu, hi = ((w0 >> 4) ^ flip) & 0x0F0F0F0Fu;
+        lo = (w0 ^ flip) & 0x0F0F0F0Fu;
+        hi = ((w0 >> 4) ^ flip) & 0x0F0F0F0Fu;
+    } else {
+        lo = w0 ^ flip;
+        hi = w1 ^ flip;
+    }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 4; ++j) {
+        uint32_t q;
+        if constexpr (BITS == 4) {
             // bytes [lo.j, 0, hi.j, 0]: selector 8 | x replicates the (zero) sign bit, which the
             // PTX instruction does and __byte_perm does not
             const uint32_t sel = (uint32_t)j | 0x80u | ((uint32_t)(4 + j) << 8) | 0xC000u;
-            uint32_t q;
             asm("prmt.b32 %0, %1, %2, %3;" : "=r"(q) : "r"(lo), "r"(hi), "r"(sel));
-            out[j] = bf16x2_mul(bf16x2_fma(q, 0x7F007F00u, zz), ss);
+        } else {
+            q = __byte_perm(j < 2 ? lo : hi, 0u, (j & 1) ? 0x4342u : 0x4140u);
         }
-    } else {
-        const float s = __uint_as_float(ss & 0xFFFF0000u), zoff = __uint_as_float(zz);
-        const uint32_t w[2] = {w0 ^ flip, w1 ^ flip};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float f[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f[i] = (__uint_as_float(__byte_perm(w[h], 0x4B000000u, 0x7540u + (uint32_t)i)) - zoff) * s;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out[2 * h]) : "f"(f[1]), "f"(f[0]));
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out[2 * h + 1]) : "f"(f[3]), "f"(f[2]));
-        }
+        out[j] = bf16x2_mul(bf16x2_fma(q, 0x7F007F00u, zz), ss);
     }
 }
 
@@ -994,9 +988,9 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
                             const bool up = vec && (ga & 2) != 0;
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                sc[j][0] = sc[j][1] = pair_scale<BITS>(__byte_perm(up ? cur[0][j].y : cur[0][j].x, 0u, sel));
+                                sc[j][0] = sc[j][1] = pair_scale(__byte_perm(up ? cur[0][j].y : cur[0][j].x, 0u, sel));
                                 zc[j][0] = zc[j][1] =
-                                    pair_zero<BITS>(__byte_perm(up ? cur[1][j].y : cur[1][j].x, 0u, sel), sym, a.zsym);
+                                    pair_zero<BITS>(__byte_perm(up ? cur[1][j].y : cur[1][j].x, 0u, sel), sym);
                             }
                             if (gb != ga) {
                                 // (g = 32: ga is even, gb the other half of the same word)
@@ -1004,8 +998,8 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
                                 for (int j = 0; j < 2; ++j) {
                                     const uint32_t sw = vec ? (up ? cur[0][j].y : cur[0][j].x) >> 16 : cur[0][j].y;
                                     const uint32_t zw = vec ? (up ? cur[1][j].y : cur[1][j].x) >> 16 : cur[1][j].y;
-                                    sc[j][1] = pair_scale<BITS>(dup16(sw));
-                                    zc[j][1] = pair_zero<BITS>(dup16(zw), sym, a.zsym);
+                                    sc[j][1] = pair_scale(dup16(sw));
+                                    zc[j][1] = pair_zero<BITS>(dup16(zw), sym);
                                 }
                             }
                             have = ga;
@@ -1098,8 +1092,8 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
                         for (int t = 0; t < 4; ++t) {
                             const uint32_t sv = pieces == 4 ? sa[t] : (pieces == 2 ? sa[t >> 1] : sa[0]);
                             const uint32_t zv = pieces == 4 ? za[t] : (pieces == 2 ? za[t >> 1] : za[0]);
-                            sc[t] = pair_scale<BITS>(dup16(sv));
-                            zc[t] = pair_zero<BITS>(dup16(zv), sym, a.zsym);
+                            sc[t] = pair_scale(dup16(sv));
+                            zc[t] = pair_zero<BITS>(dup16(zv), sym);
                         }
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {

@@ -200,7 +200,6 @@ void fill_weight_args(PairArgs* a, const Weights* w, int count, int64_t K, int32
     a->gshift = group_shift(g, K);
     a->groups = per_channel(g, K) ? 1 : (int)(K / g);
     a->flip = sym ? (bits == 4 ? 0x88888888u : 0x80808080u) : 0u;
-    a->zsym = sym ? (bits == 4 ? 8.0f : 128.0f) : 0.0f;
 }
 
 // dX [M, K] = Σ_p dY_p·Ŵ_p, dY_p rows of `ld` elements (a multiple of 8).

@@ -84,6 +84,12 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     return d;
 }
 
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
 // bf16x2 holding (128 + z, 128 + z) for an asymmetric zero point stored as bf16
 // bits (an integer 0..15), or (136, 136) for symmetric codes.
 template <bool SYM>

@@ -373,12 +373,6 @@ __device__ __forceinline__ bool pair_wait_flag(const uint64_t* flag) {
     }
 }
 
-__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-
 // A scale and zero point as the dequantization wants them, from bf16 pairs (s, s), (z, z):
 // s·2^6 and −z·2^-6 (see below; exact while s < 2^122).  Symmetric codes are flipped to
 // offset form and take z = 8 or 128.

@@ -347,18 +347,15 @@ __device__ __forceinline__ void decode_store_gated(const DecodeArgs& a, const fl
 }
 
 // Four 8-bit codes of a word -> (q0, q1) and (q2, q3) as bf16 pairs of
-// bf16_rn((q − z)·s).  The byte placed in a binary32 mantissa gives 2^23 + q
-// exactly; subtracting zoff = 2^23 + z leaves q − z (exact), the product with s
-// is exact (8-bit by 8-bit significands), and cvt.rn.bf16x2 rounds once.
-// Symmetric words are XORed with 0x80808080 by the caller (offset-128 codes,
-// zoff = 2^23 + 128).
-__device__ __forceinline__ void dq_word8(uint32_t w, float s, float zoff, uint32_t& lo, uint32_t& hi) {
-    float f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        f[i] = (__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7540u + (uint32_t)i)) - zoff) * s;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(f[1]), "f"(f[0]));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(f[3]), "f"(f[2]));
+// bf16_rn((q − z)·s).  A byte q alone in a 16-bit half is, as bf16, q·2^-133 exactly
+// (subnormal, or in the first normal binade, which continues the same steps); one fma
+// with 2^127 and nz = −z·2^-6 gives (q − z)·2^-6 exactly (an integer of at most 8 bits),
+// and the product with s6 = s·2^6 rounds (q − z)·s once (exact while s < 2^122).  Six
+// instructions; placing bytes in binary32 mantissas took fourteen.  Symmetric words are
+// XORed with 0x80808080 by the caller (offset-128 codes, nz = −2).
+__device__ __forceinline__ void dq_word8(uint32_t w, uint32_t s6, uint32_t nz, uint32_t& lo, uint32_t& hi) {
+    lo = bf16x2_mul(bf16x2_fma(__byte_perm(w, 0u, 0x4140u), 0x7F007F00u, nz), s6);
+    hi = bf16x2_mul(bf16x2_fma(__byte_perm(w, 0u, 0x4342u), 0x7F007F00u, nz), s6);
 }
 
 template <int MB, bool SYM, int G, int BITS, bool GATED = false>
@@ -863,15 +860,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     }
                 }
                 } else {
-                    // 8-bit codes: one scale group per lane and unit; s and 2^23 + z in binary32
-                    float sf[2], zf[2];
+                    // 8-bit codes: one scale group per lane and unit; pairs of s·2^6 and −z·2^-6
+                    uint32_t sf[2], zf[2];
 #pragma unroll
                     for (int hr = 0; hr < 2; ++hr) {
                         const uint8_t* sr = sb + sgrp0 * 2 + hr * srow8;
-                        sf[hr] = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(sr));
-                        zf[hr] = SYM ? 8388736.0f
-                                     : 8388608.0f + bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(
-                                                        sr + (tma_slab ? kDecSlabArrayBytes : kSzArray)));
+                        sf[hr] = bf16x2_mul(__byte_perm((uint32_t)*reinterpret_cast<const uint16_t*>(sr), 0, 0x1010), 0x42804280u);
+                        zf[hr] = SYM ? 0xC000C000u
+                                     : bf16x2_mul(__byte_perm((uint32_t)*reinterpret_cast<const uint16_t*>(
+                                                                  sr + (tma_slab ? kDecSlabArrayBytes : kSzArray)),
+                                                              0, 0x1010),
+                                                  0xBC80BC80u);
                     }
                     const uint32_t flip = SYM ? 0x80808080u : 0u;
 #pragma unroll

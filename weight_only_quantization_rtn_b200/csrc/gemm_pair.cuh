@@ -572,6 +572,14 @@ struct PairTileDone {
     uint32_t tmem, stage;
 };
 
+__device__ __forceinline__ void pair_add(float (&f0)[16], float (&f1)[16], const float4 (&p)[8]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        f0[4 * e] += p[e].x; f0[4 * e + 1] += p[e].y; f0[4 * e + 2] += p[e].z; f0[4 * e + 3] += p[e].w;
+        f1[4 * e] += p[4 + e].x; f1[4 * e + 1] += p[4 + e].y; f1[4 * e + 2] += p[4 + e].z; f1[4 * e + 3] += p[4 + e].w;
+    }
+}
+
 // The epilogue of one warp: its strips of the accumulators, finished or left as a part.
 template <bool PAIR, int GROUPS, bool DGRAD>
 __device__ __forceinline__ bool pair_epilogue(const PairArgs& a, const PairTileDone& t, int rank, int w) {
@@ -625,15 +633,26 @@ __device__ __forceinline__ bool pair_epilogue(const PairArgs& a, const PairTileD
             }
             continue;
         }
-        for (int c = t.slot + 1; c < t.followers_end; ++c) {
-            const float4* part =
-                reinterpret_cast<const float4*>(a.partials + ((int64_t)c * kCtas + rank) * part_floats + in_part);
+        // the followers' parts in order, two in flight at a time
+        const float4* part =
+            reinterpret_cast<const float4*>(a.partials + ((int64_t)(t.slot + 1) * kCtas + rank) * part_floats + in_part) + lane;
+        const int64_t next_part = kCtas * part_floats / 4;
+        int left = t.followers_end - t.slot - 1;
+        for (; left > 1; left -= 2, part += 2 * next_part) {
+            float4 p[8], q[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float4 p = __ldcg(part + e * 32 + lane), q = __ldcg(part + (4 + e) * 32 + lane);
-                f0[4 * e] += p.x; f0[4 * e + 1] += p.y; f0[4 * e + 2] += p.z; f0[4 * e + 3] += p.w;
-                f1[4 * e] += q.x; f1[4 * e + 1] += q.y; f1[4 * e + 2] += q.z; f1[4 * e + 3] += q.w;
+            for (int e = 0; e < 8; ++e) {
+                p[e] = __ldcg(part + e * 32);
+                q[e] = __ldcg(part + next_part + e * 32);
             }
+            pair_add(f0, f1, p);
+            pair_add(f0, f1, q);
+        }
+        if (left > 0) {
+            float4 p[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = __ldcg(part + e * 32);
+            pair_add(f0, f1, p);
         }
         pair_emit<DGRAD>(a, f0, f1, t.stage, t.r0, rank, quarter, t.m0 + 16 * sidx, lane);
     }

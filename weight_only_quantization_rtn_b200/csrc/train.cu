@@ -79,17 +79,19 @@ struct PairPlan {
 // of at most 256 for a pair, in steps of 16.
 //
 // Split: whole tiles in waves leave CTAs idle in the last one.  Dividing all units evenly
-// ends that, and costs each CTA writing a part and reading one, and the sharing of
-// operands in L2 between CTAs that work side by side.  Waves that are three quarters full are
-// left whole (M = 2048, 64 and 344 tiles on 74 pairs: 292 and 274 us whole, 306 and 284 us
-// split; 16 tiles: 285 us whole, 101 us split); below that both times are estimated: a block
-// takes about 0.55 us per 256 tokens and at least 0.3 us (dequantization), a CTA moves a part
-// at about 80 GB/s, and 2 us go to the flags.
+// ends that, and costs each CTA writing a part, the tiles' first owners reading those of the
+// others one after another, and the sharing of operands in L2 between CTAs that work side by
+// side.  Pairs draw the power limit either way, so their waves are left whole from three
+// quarters full on (M = 2048, 64 and 344 tiles on 74 pairs: 292 and 274 us whole, 306 and
+// 284 us split; 16 tiles: 285 us whole, 101 us split), single CTAs' from nine tenths.  Below
+// that the time is estimated for 1, 2, 3, ... sharers of each tile and for all CTAs, and the
+// least is taken: a block takes about 0.55 us per 256 tokens and at least 0.5 us
+// (dequantization), a CTA writes or reads a part at about 80 GB/s, and 2 us go to the flags.
 PairPlan pair_plan(int64_t M, int64_t rows, int rows_per_cta, int64_t blocks, int unit_blocks, int sm_count) {
     PairPlan p{};
     p.ctas = M > kPairMaxSingle ? 2 : 1;
-    const int64_t most = p.ctas == 2 ? 256 : kPairMaxSingle;
-    const int64_t tiles_m = (M + most - 1) / most;
+    const int64_t widest = p.ctas == 2 ? 256 : kPairMaxSingle;
+    const int64_t tiles_m = (M + widest - 1) / widest;
     const int64_t tokens = tiles_m > 0 ? ((M + tiles_m - 1) / tiles_m + 15) / 16 * 16 : 16;
     p.bt = (int)(tokens / p.ctas);
     p.tiles_m = (int)tiles_m;
@@ -98,15 +100,25 @@ PairPlan pair_plan(int64_t M, int64_t rows, int rows_per_cta, int64_t blocks, in
     const int64_t units = (blocks + unit_blocks - 1) / unit_blocks;
     const int64_t slots = sm_count / p.ctas;
     p.grid = (int)(p.tiles < slots ? p.tiles : slots);
-    int64_t sharers = p.tiles * units / 2;             // two units at least for each
-    if (sharers > slots) sharers = slots;
     const int64_t waves = (p.tiles + slots - 1) / slots;
-    if (4 * p.tiles < 3 * waves * slots) {
+    if (p.ctas == 2 ? 4 * p.tiles < 3 * waves * slots : 10 * p.tiles < 9 * waves * slots) {
         const int64_t part = pair_part_floats((int)tokens) * 4;
-        const double block_us = tokens * 0.55 / 256 > 0.3 ? tokens * 0.55 / 256 : 0.3;
-        const double whole = (double)waves * blocks * block_us;
-        const double split = (double)p.tiles * blocks * block_us / (double)sharers + 2.0 + 2.0 * part / 80e3;
-        if (sharers >= p.grid && split < whole) {
+        const double part_us = (double)part / 80e3;
+        const double block_us = tokens * 0.55 / 256 > 0.5 ? tokens * 0.55 / 256 : 0.5;
+        int64_t most = p.tiles * units / 2;            // two units at least for each
+        if (most > slots) most = slots;
+        int64_t sharers = 0;
+        double least = (double)(waves * blocks) * block_us;
+        for (int64_t n = 2; waves == 1 && n * p.tiles <= most; ++n) {
+            const double us = (double)((units + n - 1) / n * unit_blocks) * block_us + 2.0 + (double)n * part_us;
+            if (us < least) least = us, sharers = n * p.tiles;
+        }
+        if (most >= p.grid) {
+            const int64_t reads = (most + p.tiles - 1) / p.tiles;
+            const double us = (double)(p.tiles * blocks) * block_us / (double)most + 2.0 + (double)(1 + reads) * part_us;
+            if (us < least) least = us, sharers = most;
+        }
+        if (sharers > 0) {
             p.split = 1;
             p.grid = (int)sharers;
             p.flag_bytes = round256(sharers * p.ctas * kPairMaxWarps * 8);

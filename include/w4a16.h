@@ -448,7 +448,7 @@ w4a16_status w4a16_gemm_wgrad(const void* dY, const void* X, int64_t M, int64_t 
                               void* dW, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Embedding from a quantized table [V, K]: out[t, :] = bf16_rn(scale·Ŵ[ids[t], :]).
- *   ids in int32 or int64 [T] (id_bytes 4 or 8); out bf16 [T, K].
+ *   ids in int32 or int64 [T] (id_bytes 4 or 8), aligned to id_bytes; out bf16 [T, K].
  * An id below 0 is padding and gives a row of zeros.  An id not below V gives a row of
  * zeros too and sets the device error word to W4A16_DEVERR_ID. */
 w4a16_status w4a16_embedding(const void* ids, int32_t id_bytes, int64_t T, const void* packed,
@@ -464,7 +464,7 @@ size_t w4a16_embedding_grad_workspace_size(int64_t T, int64_t V, int64_t K);
 /* Gradient of the dense table [V, K] behind an embedding (straight through the
  * quantizer): dW[v, :] = scale·Σ_{t: ids[t] = v} dY[t, :], summed in binary32 over the
  * tokens sorted by id, in a fixed order; rows that no token names are written as zeros.
- *   dY bf16 [T, K], K a multiple of 32; dW out [V, K], binary32 (f32 = 1) or bf16 (0).
+ *   dY bf16 [T, K], K a multiple of 32; ids as above; dW out [V, K], binary32 (f32 = 1) or bf16 (0).
  * Ids below 0 are padding and add nothing; so do ids not below V, which set the device
  * error word to W4A16_DEVERR_ID. */
 w4a16_status w4a16_embedding_grad(const void* dY, const void* ids, int32_t id_bytes, int64_t T,

@@ -63,7 +63,8 @@ __device__ __forceinline__ void act_value_grad(int kind, float x, float& a, floa
         const float c = sigmoid_f32(2.0f * tanh_arg(x));          // (1 + t)/2
         a = x * c;
         // (1 − t²)/2 = 2·c·(1 − c)
-        d = c + x * (2.0f * c * (1.0f - c)) * (0.7978845608028654f * (1.0f + 0.134145f * x * x));
+        // (x² bounded: far out the middle factor is 0, and 0·inf would be a NaN)
+        d = c + x * (2.0f * c * (1.0f - c)) * (0.7978845608028654f * (1.0f + 0.134145f * fminf(x * x, 1e30f)));
     } else {
         a = x != x ? x : fmaxf(x, 0.0f);
         d = x > 0.0f ? 1.0f : 0.0f;

@@ -701,7 +701,11 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)cluster_ctarank() : 0;
-    const int slots = (int)gridDim.x / kCtas, slot = (int)blockIdx.x / kCtas;
+    // Split: shares are numbered from the last CTA to the first, so that a first owner waits for
+    // CTAs of lower index only, which are on the machine before it: however few SMs other
+    // work leaves, every wait ends.
+    const int slots = (int)gridDim.x / kCtas;
+    const int slot = a.split ? slots - 1 - (int)blockIdx.x / kCtas : (int)blockIdx.x / kCtas;
     const int per_product = a.blocks / a.products;
     const int mma_n = kCtas * a.bt;
 

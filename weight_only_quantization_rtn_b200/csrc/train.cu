@@ -34,6 +34,9 @@ w4a16_status encode_rows(CUtensorMap* map, CUtensorMapDataType dtype, const void
     return r == CUDA_SUCCESS ? W4A16_OK : W4A16_ECUDA;
 }
 
+// Ids are read one by one, so a list may begin at any of them.
+bool aligned_to(const void* p, int32_t bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
+
 bool valid_act(int32_t act) { return act >= W4A16_ACT_SILU && act <= W4A16_ACT_RELU; }
 
 int64_t round256(int64_t b) { return (b + 255) / 256 * 256; }
@@ -525,7 +528,7 @@ w4a16_status embedding_impl(const void* ids, int32_t id_bytes, int64_t T, const 
     if (st != W4A16_OK) return st;
     if (id_bytes != 4 && id_bytes != 8) return W4A16_EINVAL;
     if (T == 0) return W4A16_OK;
-    if (!ids || !out || !aligned16(ids) || !aligned16(out)) return W4A16_EINVAL;
+    if (!ids || !out || !aligned_to(ids, id_bytes) || !aligned16(out)) return W4A16_EINVAL;
     if (V > 0 && !weights_ok(w, sym)) return W4A16_EINVAL;
     DeviceInfo di;
     if ((st = device_info(&di)) != W4A16_OK) return st;
@@ -805,7 +808,7 @@ w4a16_status w4a16_embedding_grad(const void* dY, const void* ids, int32_t id_by
     if (!embed_grad_ok(T, V, K) || (id_bytes != 4 && id_bytes != 8) || (f32 != 0 && f32 != 1)) return W4A16_EINVAL;
     if (V == 0) return W4A16_OK;
     if (!dW || !aligned16(dW)) return W4A16_EINVAL;
-    if (T > 0 && (!dY || !ids || !aligned16(dY) || !aligned16(ids))) return W4A16_EINVAL;
+    if (T > 0 && (!dY || !ids || !aligned16(dY) || !aligned_to(ids, id_bytes))) return W4A16_EINVAL;
     const size_t need = w4a16_embedding_grad_workspace_size(T, V, K);
     if (workspace_bytes < need) return W4A16_EWORKSPACE;
     if (need > 0 && (!workspace || !aligned16(workspace))) return W4A16_EINVAL;

@@ -307,9 +307,9 @@ w4a16_status w8a16_gemm_plan(int64_t M, int64_t N, int64_t K, int32_t g, int32_t
  * formed on chip, binary32 accumulation, one rounding of each output to bf16;
  * deterministic.  M ≤ 16: the decode kernel with 8-bit codes (units of 256
  * rows x 128 K, i.e. the same 32 KB TMA tiles; each word of 4 codes becomes two
- * bf16 pairs — the byte in a binary32 mantissa, 2^23 + z subtracted, the exact
- * product with s rounded once — and feeds one mma.sync; split row blocks are
- * finished in the kernel, as for INT4).  M > 16: the tensor-core kernel with 8-bit
+ * bf16 pairs — the code as a subnormal bf16 number, one exact fma to (q − z)·2^-6, the
+ * product with s·2^6 rounded once; s below 2^122 — and feeds one mma.sync; split row
+ * blocks are finished in the kernel, as for INT4).  M > 16: the tensor-core kernel with 8-bit
  * codes (64-byte code rows per K block, binary32-exact dequantization into the
  * shared-memory A tile, tcgen05 MMA), split-K as for INT4.  workspace: at least
  * w8a16_gemm_workspace_size() bytes, 16-byte aligned, when that is nonzero;
@@ -361,6 +361,7 @@ w4a16_status w8a8_gemm(const void* qx, const void* sx, int64_t M, int64_t K, con
  * Quantized weights are those of w4a16_quantize (w8a16_quantize for the w8a16_
  * forms): same layouts, g and K rules, alignment, stream and error conventions as
  * above, and the weight they stand for is the same Ŵ = bf16_rn((q − z)·s).
+ * Scales are below 2^122 (those of weights up to about 2^125 are).
  * Every product is accumulated in binary32.  Results are deterministic.  Every
  * workspace is scratch: calls that may run at the same time (two streams, two
  * captured graphs) need two.

@@ -389,8 +389,9 @@ __device__ __forceinline__ uint32_t pair_zero(uint32_t zz, bool sym) {
 // in the first normal binade, which continues the same steps).  One fma with 2^127 and
 // −z·2^-6 gives (q − z)·2^-6 exactly (an integer of at most 8 bits), one multiplication by
 // s·2^6 rounds (q − z)·s once.  PRMT brings the codes into the halves: 4 bits (w0) from
-// two words of nibbles split into bytes, 8 bits (w0, w1) from the bytes themselves.  15 (4
-// bits) and 14 (8 bits) instructions; with the exponent set by a LOP3 and a subtraction 17,
+// the two nibbles of each byte, masked where they are (the upper one is 16·q and takes 2^123),
+// 8 bits (w0, w1) from the bytes themselves.  14 instructions; with the exponent set by a
+// LOP3 and a subtraction 17 for 4 bits,
 // and with 8-bit codes formed in binary32 30, which paced the kernel.
 template <int BITS>
 __device__ __forceinline__ void pair_dequant8(uint32_t w0, uint32_t w1, uint32_t flip, uint32_t zz,
@@ -398,7 +399,7 @@ __device__ __forceinline__ void pair_dequant8(uint32_t w0, uint32_t w1, uint32_t
     uint32_t lo, hi;
     if constexpr (BITS == 4) {
         lo = (w0 ^ flip) & 0x0F0F0F0Fu;
-        hi = ((w0 >> 4) ^ flip) & 0x0F0F0F0Fu;
+        hi = (w0 ^ flip) & 0xF0F0F0F0u;          // 16·q, as bf16 16·q·2^-133
     } else {
         lo = w0 ^ flip;
         hi = w1 ^ flip;
@@ -407,14 +408,14 @@ __device__ __forceinline__ void pair_dequant8(uint32_t w0, uint32_t w1, uint32_t
     for (int j = 0; j < 4; ++j) {
         uint32_t q;
         if constexpr (BITS == 4) {
-            // bytes [lo.j, 0, hi.j, 0]: selector 8 | x replicates the (zero) sign bit, which the
-            // PTX instruction does and __byte_perm does not
-            const uint32_t sel = (uint32_t)j | 0x80u | ((uint32_t)(4 + j) << 8) | 0xC000u;
+            // bytes [lo.j, 0, hi.j, 0]: selector 8 | x replicates byte x's sign bit (of a byte of
+            // lo: zero), which the PTX instruction does and __byte_perm does not
+            const uint32_t sel = (uint32_t)j | 0x80u | ((uint32_t)(4 + j) << 8) | 0x8000u;
             asm("prmt.b32 %0, %1, %2, %3;" : "=r"(q) : "r"(lo), "r"(hi), "r"(sel));
         } else {
             q = __byte_perm(j < 2 ? lo : hi, 0u, (j & 1) ? 0x4342u : 0x4140u);
         }
-        out[j] = bf16x2_mul(bf16x2_fma(q, 0x7F007F00u, zz), ss);
+        out[j] = bf16x2_mul(bf16x2_fma(q, BITS == 4 ? 0x7D007F00u : 0x7F007F00u, zz), ss);
     }
 }
 

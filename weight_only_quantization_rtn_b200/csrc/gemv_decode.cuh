@@ -358,6 +358,20 @@ __device__ __forceinline__ void dq_word8(uint32_t w, uint32_t s6, uint32_t nz, u
     hi = bf16x2_mul(bf16x2_fma(__byte_perm(w, 0u, 0x4342u), 0x7F007F00u, nz), s6);
 }
 
+// GATED, 4 bits: the same for the nibble pair at bits 4·POS of each half (POS 0 or 1).  At bits
+// 4..7 a nibble is 16·q·2^-133, still exact, and 2^123 brings it to the same q·2^-6, so
+// one shift serves two pairs: 13 instructions a word, where the pattern 128 + q (which
+// has room for the low nibble only) takes 15.  Symmetric codes are flipped in the same LOP3.
+template <bool SYM, int POS>
+__device__ __forceinline__ uint32_t dq_pair4(uint32_t w, uint32_t mask, uint32_t nz, uint32_t s6) {
+    uint32_t c;
+    if constexpr (SYM)
+        asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(c) : "r"(w), "r"(mask), "n"(POS ? 0x00800080 : 0x00080008));
+    else
+        c = w & mask;
+    return bf16x2_mul(bf16x2_fma(c, POS ? 0x7D007D00u : 0x7F007F00u, nz), s6);
+}
+
 template <int MB, bool SYM, int G, int BITS, bool GATED = false>
 __global__ void __launch_bounds__(kDecThreads, 1)
     gemv_decode_kernel(const __grid_constant__ DecodeMaps<GATED> maps, const DecodeArgs a) {
@@ -733,7 +747,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     uint32_t slab_ph = 1u;                           // parity of its use of the slot
     const uint8_t* slab_ptr = slab_base;
     const uint32_t nib = opaque_u32(0x000F000Fu);     // nibble-pair mask, held in a register
-    const uint32_t zz_sym = opaque_u32(0x43084308u);  // 128 + 8 for symmetric codes
+    const uint32_t nib4 = GATED ? opaque_u32(0x00F000F0u) : 0u;
+    // symmetric codes: 128 + 8 (GATED: −8·2^-6)
+    const uint32_t zz_sym = opaque_u32(GATED ? 0xBE00BE00u : 0x43084308u);
 
     float acc[2][MB][4];
 #pragma unroll
@@ -814,11 +830,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     for (int hr = 0; hr < 2; ++hr) {
                         const uint8_t* sr = sh + hr * srow8;
                         ss[h][hr] = __byte_perm((uint32_t)*reinterpret_cast<const uint16_t*>(sr), 0, 0x1010);
-                        zz[h][hr] = SYM ? zz_sym
-                                        : bf16x2_add(__byte_perm((uint32_t)*reinterpret_cast<const uint16_t*>(
-                                                                     sr + (tma_slab ? kDecSlabArrayBytes : kSzArray)),
-                                                                 0, 0x1010),
-                                                     0x43004300u);
+                        zz[h][hr] = zz_sym;
+                        if (!SYM) {
+                            const uint32_t z = __byte_perm((uint32_t)*reinterpret_cast<const uint16_t*>(
+                                                               sr + (tma_slab ? kDecSlabArrayBytes : kSzArray)),
+                                                           0, 0x1010);
+                            zz[h][hr] = GATED ? bf16x2_mul(z, 0xBC80BC80u) : bf16x2_add(z, 0x43004300u);
+                        }
+                        if (GATED) ss[h][hr] = bf16x2_mul(ss[h][hr], 0x42804280u);
                     }
                 }
                 if (G != 32) {
@@ -844,10 +863,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                         for (int hh = 0; hh < 2; ++hh) {
                             // fragment registers in the order the MMA reads them:
                             // (row g, k-pair lo) (row g+8, lo) (row g, hi) (row g+8, hi)
-                            const uint32_t f0 = dq_pair_m<SYM>(w0[ii] >> (8 * hh), nib, zz[h][0], ss[h][0]);
-                            const uint32_t f1 = dq_pair_m<SYM>(w1[ii] >> (8 * hh), nib, zz[h][1], ss[h][1]);
-                            const uint32_t f2 = dq_pair_m<SYM>(w0[ii] >> (8 * hh + 4), nib, zz[h][0], ss[h][0]);
-                            const uint32_t f3 = dq_pair_m<SYM>(w1[ii] >> (8 * hh + 4), nib, zz[h][1], ss[h][1]);
+                            uint32_t f0, f1, f2, f3;
+                            if constexpr (GATED) {
+                                f0 = dq_pair4<SYM, 0>(w0[ii] >> (8 * hh), nib, zz[h][0], ss[h][0]);
+                                f1 = dq_pair4<SYM, 0>(w1[ii] >> (8 * hh), nib, zz[h][1], ss[h][1]);
+                                f2 = dq_pair4<SYM, 1>(w0[ii] >> (8 * hh), nib4, zz[h][0], ss[h][0]);
+                                f3 = dq_pair4<SYM, 1>(w1[ii] >> (8 * hh), nib4, zz[h][1], ss[h][1]);
+                            } else {
+                                f0 = dq_pair_m<SYM>(w0[ii] >> (8 * hh), nib, zz[h][0], ss[h][0]);
+                                f1 = dq_pair_m<SYM>(w1[ii] >> (8 * hh), nib, zz[h][1], ss[h][1]);
+                                f2 = dq_pair_m<SYM>(w0[ii] >> (8 * hh + 4), nib, zz[h][0], ss[h][0]);
+                                f3 = dq_pair_m<SYM>(w1[ii] >> (8 * hh + 4), nib, zz[h][1], ss[h][1]);
+                            }
                             const uint32_t b0 = hh == 0 ? xv0[ii].x : xv0[ii].z;
                             const uint32_t b1 = hh == 0 ? xv0[ii].y : xv0[ii].w;
                             mma_bf16_16816_nv(acc[hh][0], f0, f1, f2, f3, b0, b1);

@@ -155,6 +155,29 @@ __device__ __forceinline__ void dequant8_natural(uint32_t w, uint32_t zz, uint32
     }
 }
 
+// ------------------------------------------------------------------ asynchronous copies
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes) {
+    // 4-byte async copy global -> shared; bytes beyond src_bytes (0 or 4) are zero-filled.
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, uint32_t src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t src_bytes) {
+    // 16-byte async copy global -> shared; bytes beyond src_bytes (0..16) are zero-filled.
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void cp_async_arrive_noinc(uint32_t bar) {
+    // Arrive on the barrier once this thread's earlier cp.async copies have landed.
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // ------------------------------------------------------------------ warp MMA (decode path)
 // D[16x8] += A[16x16] · B[16x8], bf16 inputs, fp32 accumulators.
 __device__ __forceinline__ void mma_bf16_16816(float c[4], uint32_t a0, uint32_t a1, uint32_t a2,

@@ -26,14 +26,14 @@
 // tensor core reads as the transposed A operand; nothing is transposed in memory.
 //
 // Warps: 0 loads tokens (TMA, 128-byte swizzle), 2 loads codes (TMA), 1 issues the MMAs
-// and owns the tensor memory, 4 and up dequantize and run the epilogue (8 or 12, so that a
-// thread has 168 or 128 registers; sixteen of 96 spilled and were slower).  Three rings of
+// and owns the tensor memory, 3 brings scales and zero points (GATED), 4 and up dequantize and
+// run the epilogue (8, 12 or 16 warps: 168, 128 or 96 registers).  Three rings of
 // shared memory, because the three have different sizes and lead times: token blocks,
 // code units (GATED with 4 bits: 128 input channels, so that a row is 64 bytes; loaded as
 // 32-byte rows the TMA engine's row rate, not bandwidth, paced the kernel) and dequantized
-// A tiles.  Scales and zero points go from global memory to registers
-// ahead of their block, so any number of groups per row and any alignment is read the
-// same way.
+// A tiles.  Scales and zero points of GATED have a small ring of their own, four groups
+// a slot; DGRAD's go from global memory to registers two blocks ahead.  Both read rows of any
+// number of groups and any alignment.
 //
 // The kernel is persistent, one CTA (or pair) per SM (or two).  Either whole tiles are
 // dealt in turn, or (when that would leave CTAs idle for longer than it costs) all tiles'
@@ -213,16 +213,20 @@ constexpr uint32_t kIdescBMnMajor = 1u << 16;
 
 // ------------------------------------------------------------------ configuration
 constexpr int kPairCodeWarp = 2;
+constexpr int kPairScaleWarp = 3;       // GATED
 constexpr int kPairBlock = 64;          // reduction per block
 constexpr int kPairRows = 128;          // rows of one A tile per CTA
 constexpr int kPairABytes = 2 * kPairRows * kPairBlock * 2;   // both A tiles of a block: 32 KB
+constexpr int kPairQuadBytes = 2 * 2 * kPairRows * 8;        // four groups' [scale, zero][matrix][row]: 4 KB
+constexpr int kPairMaxQuads = 4;
 constexpr int kPairMaxX = 8;
-constexpr int kPairMaxWarps = 12;       // dequantizing warps, at most
+constexpr int kPairMaxWarps = 16;       // dequantizing warps, at most
 
 // A pair's MMAs take longer than two groups of dequantizing warps need for a block; a single
 // CTA's small tiles do not, so its 4-bit gradient has a third group (M = 77, K = 37888,
-// N = 8192: 157 us with two groups, 133 us with three).  Three gained nothing with 8-bit codes
-// and spilled in the gated form (M = 61, K = 4096, N = 11008: 37.8 us with two, 40.3 with three).
+// N = 8192: 157 us with two groups, 133 us with three); three gained nothing with 8-bit codes.
+// With kTmemA a group costs no A buffer and 96 registers do, so there are four (M = 61,
+// K = 8192, N = 18944: 66.6 us with two, 60.7 with three, 56.1 with four).
 //
 // kTmemA: a single CTA's GATED tiles leave tensor memory free, and what paced them with the A
 // tiles in shared memory was its bandwidth (0.57 us per block at any token count, 0.39 us
@@ -233,13 +237,15 @@ constexpr int kPairMaxA = 6;
 template <bool PAIR, int BITS, bool DGRAD>
 struct PairConfig {
     static constexpr bool kTmemA = !PAIR && !DGRAD;
-    static constexpr int kGroups = !PAIR && DGRAD && BITS == 4 ? 3 : 2;
+    static constexpr int kGroups = kTmemA ? 4 : (!PAIR && DGRAD && BITS == 4 ? 3 : 2);
     static constexpr int kWarps = 4 * kGroups;                 // warps 4 .. 4 + kWarps - 1
     static constexpr int kThreads = (4 + kWarps) * 32;
     static constexpr int kSmemA = kTmemA ? 0 : (kGroups + 1) * kPairABytes;   // A ring
     static constexpr int kStage = kWarps * 1024;               // epilogue staging, 1 KB per warp
-    static constexpr int kLoads = kTmemA ? 225 * 1024 - kStage : (kGroups == 2 ? 112 * 1024 : 84 * 1024);
-    static constexpr int kSmem = kSmemA + kStage + kLoads + 1024 + 1024;
+    static constexpr int kQuads = DGRAD ? 0 : (kTmemA ? 4 : 2);  // ring of scales, four groups a slot
+    static constexpr int kLoads = kTmemA ? 225 * 1024 - kStage - kQuads * kPairQuadBytes
+                                         : (kGroups == 2 ? 112 * 1024 : 84 * 1024);
+    static constexpr int kSmem = kSmemA + kStage + kQuads * kPairQuadBytes + kLoads + 1024 + 1024;
     static_assert(kSmem <= 232448, "shared memory");
     // 64-wide blocks per code unit, and its bytes: two boxes (gate, up) of 128 rows, of 128 bytes
     // with kTmemA and 64 bytes in a pair's tighter ring; DGRAD: 64 rows x 256 channels.
@@ -295,7 +301,7 @@ struct PairArgs {
     int tiles_m;
     int tiles;
     int split;                   // 1: the tiles' code units are divided evenly over the CTAs
-    uint64_t* flags;             // [slots][CTAs of a slot][12] ready flags of the parts
+    uint64_t* flags;             // [slots][CTAs of a slot][kPairMaxWarps] ready flags of the parts
 };
 
 // Ready flag of a part: no sum, index or bf16 data is likely to hold it, so the workspace
@@ -391,8 +397,7 @@ __device__ __forceinline__ uint32_t pair_zero(uint32_t zz, bool sym) {
 // s·2^6 rounds (q − z)·s once.  PRMT brings the codes into the halves: 4 bits (w0) from
 // the two nibbles of each byte, masked where they are (the upper one is 16·q and takes 2^123),
 // 8 bits (w0, w1) from the bytes themselves.  14 instructions; with the exponent set by a
-// LOP3 and a subtraction 17 for 4 bits,
-// and with 8-bit codes formed in binary32 30, which paced the kernel.
+// LOP3 and a subtraction 17 for 4 bits, and with 8-bit codes formed in binary32 30.
 template <int BITS>
 __device__ __forceinline__ void pair_dequant8(uint32_t w0, uint32_t w1, uint32_t flip, uint32_t zz,
                                               uint32_t ss, uint32_t out[4]) {
@@ -450,10 +455,9 @@ __device__ __forceinline__ uint4 lds128_addr(uint32_t addr) {
     return v;
 }
 
-// An 8-byte read of scales or zeros through the read-only path.
-__device__ __forceinline__ uint2 ldg_u64x(const void* p) {
-    uint2 v;
-    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
     return v;
 }
 
@@ -550,6 +554,11 @@ __device__ __forceinline__ void pair_emit(const PairArgs& a, float v0[16], float
         }
         strip_store(v0, stage, a.out, m, a.M, c, a.N, lane);
     }
+}
+
+// Scale group of half h of the reduction block (GATED).
+__device__ __forceinline__ int pair_group(const PairArgs& a, int block, int h) {
+    return min((block * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
 }
 
 // First row of a tile (features or input channels) and its first token.
@@ -692,12 +701,14 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
     const uint32_t ps = as + Cfg::kSmemA;            // SP code units
     const uint32_t xs = ps + SP * Cfg::kUnitBytes;   // SX token blocks
     const uint32_t st = ps + Cfg::kLoads;            // epilogue staging
-    const uint32_t bars = st + Cfg::kStage;
+    const uint32_t qs = st + Cfg::kStage;            // kQuads scale slots
+    const uint32_t bars = qs + Cfg::kQuads * kPairQuadBytes;
     const uint32_t xfull = bars, xempty = xfull + 8 * kPairMaxX;
     const uint32_t pfull = xempty + 8 * kPairMaxX, pempty = pfull + 8 * kPairMaxX;
     const uint32_t afull = pempty + 8 * kPairMaxX, aempty = afull + 8 * kPairMaxA;
     const uint32_t accf = aempty + 8 * kPairMaxA, accempty = accf + 8;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + (accempty + 8 - as));
+    const uint32_t qfull = accempty + 8, qempty = qfull + 8 * kPairMaxQuads;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + (qempty + 8 * kPairMaxQuads - as));
 
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int lane = threadIdx.x & 31;
@@ -722,6 +733,10 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
         for (int s = 0; s < NA; ++s) {
             mbar_init(afull + 8 * s, kCtas * 4);
             mbar_init(aempty + 8 * s, 1);
+        }
+        for (int s = 0; s < Cfg::kQuads; ++s) {
+            mbar_init(qfull + 8 * s, 32);
+            mbar_init(qempty + 8 * s, Cfg::kWarps);
         }
         mbar_init(accf, 1);
         mbar_init(accempty, kCtas * Cfg::kWarps);
@@ -864,6 +879,71 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
             if (!ok && elect_one()) tc_commit_g<PAIR>(accf);     // error: no MMA outlives the CTA
         }
         __syncwarp();
+    } else if (!DGRAD && warp == kPairScaleWarp) {
+        // ------------------------------------------------------------ scales and zeros
+        // A slot holds four consecutive groups of the tile's rows; the slots of a segment follow its
+        // reduction.  (Fetched by the dequantizing warps into registers ahead of their use,
+        // a quarter of their time went to issuing these scattered loads and to the moves
+        // that awaited them: M = 61, K = 8192, N = 18944 took 73 us instead of 66.6.)
+        if constexpr (!DGRAD) {
+            // rows of scales are aligned to 8 or 4 bytes (copied asynchronously), or to 2
+            const int align = (a.groups & 3) == 0 ? 8 : ((a.groups & 1) == 0 ? 4 : 2);
+            const int arrays = a.flip != 0u ? 1 : 2;
+            int s = 0;
+            uint32_t ph = 0;
+            bool ok = true;
+            while (ok && walk.next(a, slots)) {
+                const int b0 = walk.first_block(), last = b0 + walk.count(a) - 1;
+                const int q0 = pair_group(a, b0, 0) >> 2, q1 = pair_group(a, last, 1) >> 2;
+                const int n0 = pair_row0<DGRAD>(a, walk.tile, kCtas) + rank * kPairRows + lane;
+                int64_t row[4];                               // this lane's rows, 32 apart
+                // (a row behind the last reads the last row's scales: its results are dropped)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) row[k] = (int64_t)min(n0 + 32 * k, a.N - 1) * a.groups;
+                for (int qd = q0; qd <= q1; ++qd) {
+                    if (lane == 0) ok = mbar_wait_backoff(qempty + 8 * s, ph ^ 1u, 128u);
+                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                    if (!ok) break;
+                    const uint32_t dst = qs + (uint32_t)(s * kPairQuadBytes + 8 * lane);
+                    const bool half = 4 * qd + 2 < a.groups;   // the slot's third group exists
+                    for (int t = 0; t < arrays; ++t) {
+                        uint32_t v[2][4][4];
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const uint16_t* base = (t == 0 ? a.scales[m] : a.zeros[m]) + 4 * qd;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint16_t* src = base + row[k];
+                                const uint32_t d = dst + (uint32_t)(((2 * t + m) * kPairRows + 32 * k) * 8);
+                                if (align == 8) {
+                                    cp_async_8(d, src, 8u);
+                                } else if (align == 4) {
+                                    cp_async_4(d, src, 4u);
+                                    cp_async_4(d + 4, half ? src + 2 : src, half ? 4u : 0u);
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) v[m][k][e] = ldg_u16(src + min(e, a.groups - 1 - 4 * qd));
+                                }
+                            }
+                        }
+                        if (align == 2)
+#pragma unroll
+                            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(
+                                                     dst + (uint32_t)(((2 * t + m) * kPairRows + 32 * k) * 8)),
+                                                 "r"(v[m][k][0] | v[m][k][1] << 16), "r"(v[m][k][2] | v[m][k][3] << 16)
+                                                 : "memory");
+                    }
+                    if (align > 2) cp_async_arrive_noinc(qfull + 8 * s);
+                    else mbar_arrive(qfull + 8 * s);
+                    if (++s == Cfg::kQuads) { s = 0; ph ^= 1u; }
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");     // no copy outlives the CTA
+        }
+        __syncwarp();
     } else if (warp >= 4) {
         // ------------------------------------------------------------ dequantize, epilogue
         // Groups of four warps take the blocks in turn, so that one group's waits, fences and
@@ -873,6 +953,9 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
         const bool sym = a.flip != 0u;
         const uint32_t afull_r = PAIR ? mapa_u32(afull, 0) : afull;
         int cnt = 0, ucnt = 0, seg = 0;              // blocks and units of the segments before
+        // GATED: scale slots of the segments before, the one at hand (counted through all), its place
+        int quads = 0, quad = -1, qslot = -1;
+        uint32_t qph = 0;
         bool ok = true;
         // A finished tile's epilogue runs after the next segment's first NA blocks were
         // dequantized, while its own last MMAs complete: the pipeline is full again when the
@@ -948,76 +1031,44 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
             if constexpr (!DGRAD) {
                 // thread = row r of both matrices
                 const int r = wg * 32 + lane;
-                // (a row behind the last reads the last row's scales: its results are dropped)
-                const int n = min(r0 + rank * kPairRows + r, a.N - 1);
-                const bool vec = (a.groups & 3) == 0;         // rows of scales are 8-byte aligned
-                const int64_t srow = (int64_t)n * a.groups;
                 const uint32_t sts0 = (uint32_t)(r * 128 + ((r & 7) * 16));               // chunk c: ^ 16·c
                 // this row's codes in a unit; logical chunk c is at ^ 16·c (128- or 64-byte swizzle)
                 const uint32_t lds0 = ps + (Cfg::kTmemA ? (uint32_t)(r * 128 + (r & 7) * 16)
                                                         : (uint32_t)(r * 64 + ((r >> 1) & 3) * 16));
-                auto group_of = [&](int blk, int h) {
-                    return min(((b0 + blk) * kPairBlock + 32 * h) >> a.gshift, a.groups - 1);
+                // The slot of scales at hand: every warp walks through all of a segment's, in order,
+                // and gives one back when it goes on (what it read there was used by then).
+                const int quad0 = pair_group(a, b0, 0) >> 2;
+                auto advance = [&](int to) {
+                    while (quad < to && ok) {
+                        if (quad >= 0) {
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(qempty + 8 * qslot);
+                        }
+                        ++quad;
+                        if (++qslot == Cfg::kQuads) { qslot = 0; qph ^= 1u; }
+                        ok = mbar_wait(qfull + 8 * qslot, qph) && ok;
+                    }
                 };
-                // Scales and zeros: four groups at hand and the next four on their way, or (rows
-                // of another alignment) the two halves' groups of this block and of the next
-                // one of this warp.  [scale, zero][matrix]
-                uint2 cur[2][2], nxt[2][2];
                 uint32_t sc[2][2], zc[2][2];                  // pairs of [matrix][half of the block]
                 int have = -1;
-                auto fetch = [&](uint2 (&to)[2][2], int blk) {
-                    const int ga = group_of(blk, 0), gb = group_of(blk, 1);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            if (t == 1 && sym) continue;
-                            const uint16_t* p = (t == 0 ? a.scales[j] : a.zeros[j]) + srow;
-                            if (vec) {
-                                to[t][j] = ldg_u64x(p + (ga & ~3));
-                            } else {
-                                to[t][j].x = ldg_u16(p + ga);
-                                to[t][j].y = ldg_u16(p + gb);
-                            }
-                        }
-                };
-                // first block of this warp whose scales lie behind those at hand
-                auto beyond = [&](int blk) {
-                    if (!vec) return blk + NG;
-                    const int k = ((((group_of(blk, 0) >> 2) + 1) * 4) << a.gshift) / kPairBlock - b0;
-                    return max(blk + NG, k + (grp - k % NG + NG) % NG);
-                };
-#pragma unroll
-                for (int j = 0; j < 2; ++j) cur[0][j] = cur[1][j] = nxt[0][j] = nxt[1][j] = make_uint2(0u, 0u);
-                if (more) fetch(nxt, grp);
                 for (int phase = pending ? 0 : 1; phase < 2; ++phase) {
                     const int hi = phase == 0 ? min(nb, NA) : nb;
                     for (; i < hi && ok; i += NG) {
-                        const int ga = group_of(i, 0), gb = group_of(i, 1);
+                        const int ga = pair_group(a, b0 + i, 0), gb = pair_group(a, b0 + i, 1);
                         if (ga != have || gb != ga) {
-                            if (!vec || have < 0 || (ga >> 2) != (have >> 2)) {
-#pragma unroll
-                                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                                    for (int j = 0; j < 2; ++j) cur[t][j] = nxt[t][j];
-                                fetch(nxt, beyond(i));
-                            }
-                            const uint32_t sel = vec && (ga & 1) ? 0x3232u : 0x1010u;
-                            const bool up = vec && (ga & 2) != 0;
+                            advance(quads + (ga >> 2) - quad0);
+                            if (!ok) break;
+                            const uint32_t at = qs + (uint32_t)(qslot * kPairQuadBytes + 8 * r + 2 * (ga & 3));
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                sc[j][0] = sc[j][1] = pair_scale(__byte_perm(up ? cur[0][j].y : cur[0][j].x, 0u, sel));
-                                zc[j][0] = zc[j][1] =
-                                    pair_zero<BITS>(__byte_perm(up ? cur[1][j].y : cur[1][j].x, 0u, sel), sym);
+                                sc[j][0] = sc[j][1] = pair_scale(dup16(lds_u16(at + j * 8 * kPairRows)));
+                                zc[j][0] = zc[j][1] = pair_zero<BITS>(sym ? 0u : dup16(lds_u16(at + (2 + j) * 8 * kPairRows)), sym);
                             }
-                            if (gb != ga) {
-                                // (g = 32: ga is even, gb the other half of the same word)
+                            if (gb != ga) {                   // (g = 32: the next group, of the same four)
 #pragma unroll
                                 for (int j = 0; j < 2; ++j) {
-                                    const uint32_t sw = vec ? (up ? cur[0][j].y : cur[0][j].x) >> 16 : cur[0][j].y;
-                                    const uint32_t zw = vec ? (up ? cur[1][j].y : cur[1][j].x) >> 16 : cur[1][j].y;
-                                    sc[j][1] = pair_scale(dup16(sw));
-                                    zc[j][1] = pair_zero<BITS>(dup16(zw), sym);
+                                    sc[j][1] = pair_scale(dup16(lds_u16(at + 2 + j * 8 * kPairRows)));
+                                    zc[j][1] = pair_zero<BITS>(sym ? 0u : dup16(lds_u16(at + 2 + (2 + j) * 8 * kPairRows)), sym);
                                 }
                             }
                             have = ga;
@@ -1066,6 +1117,11 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
                         release();
                     }
                     if (phase == 0 && ok) epilogue();
+                }
+                if (more) {                                   // the segment's other slots
+                    const int n = (pair_group(a, b0 + nb - 1, 1) >> 2) - quad0 + 1;
+                    advance(quads + n - 1);
+                    quads += n;
                 }
             } else {
                 // thread = weight row r of the block, 128 channels (one A tile) q: a warp's scale

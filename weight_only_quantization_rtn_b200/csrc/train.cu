@@ -88,8 +88,9 @@ struct PairPlan {
 // quarters full on (M = 2048, 64 and 344 tiles on 74 pairs: 292 and 274 us whole, 306 and
 // 284 us split; 16 tiles: 285 us whole, 101 us split), single CTAs' from nine tenths.  Below
 // that the time is estimated for 1, 2, 3, ... sharers of each tile and for all CTAs, and the
-// least is taken: a block takes about 0.55 us per 256 tokens and at least 0.5 us
-// (dequantization), a CTA writes or reads a part at about 80 GB/s, and 2 us go to the flags.
+// least is taken: a block takes about 0.55 us per 256 tokens and at least 0.5 us, 0.35 us for a
+// single CTA (dequantization), a CTA writes or reads a part at about 80 GB/s, and 2 us go to
+// the flags (M = 61, K = 11008, N = 4096: 31 us shared, 67 us whole).
 PairPlan pair_plan(int64_t M, int64_t rows, int rows_per_cta, int64_t blocks, int unit_blocks, int sm_count) {
     PairPlan p{};
     p.ctas = M > kPairMaxSingle ? 2 : 1;
@@ -107,7 +108,8 @@ PairPlan pair_plan(int64_t M, int64_t rows, int rows_per_cta, int64_t blocks, in
     if (p.ctas == 2 ? 4 * p.tiles < 3 * waves * slots : 10 * p.tiles < 9 * waves * slots) {
         const int64_t part = pair_part_floats((int)tokens) * 4;
         const double part_us = (double)part / 80e3;
-        const double block_us = tokens * 0.55 / 256 > 0.5 ? tokens * 0.55 / 256 : 0.5;
+        const double least_us = p.ctas == 2 ? 0.5 : 0.35;
+        const double block_us = tokens * 0.55 / 256 > least_us ? tokens * 0.55 / 256 : least_us;
         int64_t most = p.tiles * units / 2;            // two units at least for each
         if (most > slots) most = slots;
         int64_t sharers = 0;

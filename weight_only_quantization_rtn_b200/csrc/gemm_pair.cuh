@@ -236,6 +236,7 @@ constexpr int kPairMaxWarps = 16;       // dequantizing warps, at most
 constexpr int kPairMaxA = 6;
 template <bool PAIR, int BITS, bool DGRAD>
 struct PairConfig {
+    static constexpr bool kPair = PAIR;
     static constexpr bool kTmemA = !PAIR && !DGRAD;
     static constexpr int kGroups = kTmemA ? 4 : (!PAIR && DGRAD && BITS == 4 ? 3 : 2);
     static constexpr int kWarps = 4 * kGroups;                 // warps 4 .. 4 + kWarps - 1
@@ -274,7 +275,10 @@ __host__ __device__ inline PairRings pair_rings(int bt, int acc_cols) {
         r.sp = (Cfg::kLoads - r.sx * x_bytes) / Cfg::kUnitBytes;
     } else {
         r.na = Cfg::kGroups + 1;
-        r.sp = (Cfg::kGroups == 2 || bt <= 64 ? 48 * 1024 : 32 * 1024) / Cfg::kUnitBytes;
+        // tokens come from L2 and need less of a lead than codes do
+        r.sx = Cfg::kPair ? r.na + 1 : r.na;
+        r.sp = (Cfg::kLoads - r.sx * x_bytes) / Cfg::kUnitBytes;
+        if (r.sp > kPairMaxX) r.sp = kPairMaxX;
         r.sx = (Cfg::kLoads - r.sp * Cfg::kUnitBytes) / x_bytes;
         if (r.sx > kPairMaxX) r.sx = kPairMaxX;
     }
@@ -1133,7 +1137,7 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
                 // (a row or channel behind the last reads the last one's pair: the tokens' values
                 // there are zeros, or the results are dropped)
                 const int pieces = a.gshift >= 7 ? 1 : (a.gshift == 6 ? 2 : 4);   // groups in 128 channels
-                const int g0 = c0 >> a.gshift, glast = a.groups - 1;
+                const int g0 = c0 >> a.gshift, glast = a.groups - 1, gfirst = min(g0, glast);
                 auto fetch = [&](int blk, uint32_t (&sb)[4], uint32_t (&zb)[4]) {
                     int b = b0 + min(blk, nb - 1);
                     const bool second = b >= per_product;
@@ -1141,8 +1145,11 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
                     const int64_t at = (int64_t)min(b * kPairBlock + r, a.N - 1) * a.groups;
                     const uint16_t* sp = (second ? a.scales[1] : a.scales[0]) + at;
                     const uint16_t* zp = (second ? a.zeros[1] : a.zeros[0]) + at;
+                    sb[0] = ldg_u16(sp + gfirst);
+                    if (!sym) zb[0] = ldg_u16(zp + gfirst);
+                    if (pieces == 1) return;
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
+                    for (int t = 1; t < 4; ++t)
                         if (t < pieces) {
                             sb[t] = ldg_u16(sp + min(g0 + t, glast));
                             if (!sym) zb[t] = ldg_u16(zp + min(g0 + t, glast));
@@ -1162,12 +1169,20 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
                     const int hi = phase == 0 ? min(nb, NA) : nb;
                     for (; i < hi && ok; i += NG) {
                         uint32_t sc[4], zc[4];                   // pairs of the four 32-channel pieces
+                        sc[0] = pair_scale(dup16(sa[0]));
+                        zc[0] = pair_zero<BITS>(dup16(za[0]), sym);
+                        if (pieces == 1) {
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const uint32_t sv = pieces == 4 ? sa[t] : (pieces == 2 ? sa[t >> 1] : sa[0]);
-                            const uint32_t zv = pieces == 4 ? za[t] : (pieces == 2 ? za[t >> 1] : za[0]);
-                            sc[t] = pair_scale(dup16(sv));
-                            zc[t] = pair_zero<BITS>(dup16(zv), sym);
+                            for (int t = 1; t < 4; ++t) {
+                                sc[t] = sc[0];
+                                zc[t] = zc[0];
+                            }
+                        } else {
+#pragma unroll
+                            for (int t = 1; t < 4; ++t) {
+                                sc[t] = pair_scale(dup16(pieces == 4 ? sa[t] : sa[t >> 1]));
+                                zc[t] = pair_zero<BITS>(dup16(pieces == 4 ? za[t] : za[t >> 1]), sym);
+                            }
                         }
 #pragma unroll
                         for (int t = 0; t < 4; ++t) {

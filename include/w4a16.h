@@ -385,9 +385,9 @@ size_t w8a16_gated_workspace_size(int64_t M, int64_t N, int64_t K, int32_t g, in
  *   X bf16 [M, K]; gate and up weights [N, K] each; H out bf16 [M, N].
  *   G, U out bf16 [M, N], both or neither (NULL): the projections, each rounded once,
  *   as w4a16_gated_backward takes them.
- *   path: w4a16_path, optionally OR'ed with W4A16_STATIC_WEIGHTS (M ≤ 16); AUTO runs
- *   the decode kernel for M ≤ 16 (every weight is read once at HBM rate), else the
- *   tensor-core kernel. */
+ *   path: w4a16_path, optionally OR'ed with W4A16_STATIC_WEIGHTS (of use to the decode
+ *   kernel); AUTO runs the decode kernel for M ≤ 16 (with matrices of more than about 10^8
+ *   weights only for M ≤ 8 and 4 bits), else the tensor-core kernel. */
 w4a16_status w4a16_gated(const void* X, int64_t M, int64_t K, const void* gate_packed,
                          const void* gate_scales, const void* gate_zeros, const void* up_packed,
                          const void* up_scales, const void* up_zeros, int64_t N, int32_t g,

@@ -229,3 +229,18 @@ def test_offsets_past_31_bits():
     assert torch.equal(dT[ids], W)
     dT[ids] = 0
     assert all(int(c.count_nonzero()) == 0 for c in dT.split(100000))
+
+
+@pytest.mark.parametrize("bits,M", [(8, 1), (8, 9), (4, 8), (4, 16)])
+def test_short_batches_of_large_matrices(bits, M):
+    """Both sides of the size from which up to 16 tokens go to the tensor cores: the path chosen
+    and the two that can be forced agree with the plain product."""
+    K, g = 2048, 128
+    for N in (49152, 49160):                                  # 96·2^20 weights, and more
+        gate, up = random_weights(N, K, g, bits, 11), random_weights(N, K, g, bits, 12)
+        X = workloads.make_activation(M, K, 13).cuda()
+        f, dq = (w4.gated, w4.dequantize) if bits == 4 else (w4.gated8, w4.dequantize8)
+        want = act64(X.double() @ dq(*gate, g=g).double().t(), "silu") * (X.double() @ dq(*up, g=g).double().t())
+        for path in ("auto", "decode", "tensorcore"):
+            H = f(X, gate, up, g=g, path=path)
+            assert_y_close(workloads.bits(H), want.cpu().numpy(), f"{bits} {M} {N} {path}")

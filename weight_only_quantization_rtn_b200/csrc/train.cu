@@ -287,12 +287,20 @@ w4a16_status launch_gated_decode_g(int gsel, int64_t grid, int smem, const Decod
     }
 }
 
-// What a gated call runs: the decode kernel for at most 16 tokens, else the tensor cores.
 // 64-wide blocks per code unit of the tensor-core kernel (PairConfig::kUnitBlocks).
 int gated_unit_blocks(int64_t M, int bits) {
     if (M > kPairMaxSingle)
         return bits == 8 ? PairConfig<true, 8, false>::kUnitBlocks : PairConfig<true, 4, false>::kUnitBlocks;
     return bits == 8 ? PairConfig<false, 8, false>::kUnitBlocks : PairConfig<false, 4, false>::kUnitBlocks;
+}
+
+// What a gated call of up to 16 tokens runs.  The decode kernel starts and ends sooner; the
+// tensor-core kernel, whatever the tokens, dequantizes faster than 8-bit codes or two blocks of
+// eight tokens do there.  They meet near 10^8 weights a matrix (4 bits, M = 16: 8192^2 33.3 us
+// decode, 33.9 tensor cores; 8192 x 28672 113.9 and 82.5; 8 bits, M = 1: 29.8 and 35.5, 104.3
+// and 88.8; 4 bits, M = 8: 81.3 and 82.7, so there it stays the decode kernel).
+bool gated_decode(int64_t M, int64_t N, int64_t K, int bits) {
+    return M <= 16 && ((bits == 4 && M <= 8) || N <= (int64_t(96) << 20) / K);
 }
 
 struct GatedPlan {
@@ -307,7 +315,7 @@ w4a16_status gated_plan(int64_t M, int64_t N, int64_t K, int32_t g, int32_t path
     if (path < W4A16_PATH_AUTO || path > W4A16_PATH_TENSORCORE) return W4A16_EINVAL;
     if (path == W4A16_PATH_DECODE && M > 16) return W4A16_EINVAL;
     GatedPlan q{};
-    q.decode = path == W4A16_PATH_DECODE || (path == W4A16_PATH_AUTO && M <= 16);
+    q.decode = path == W4A16_PATH_DECODE || (path == W4A16_PATH_AUTO && gated_decode(M, N, K, bits));
     if (N > kMaxDim / 2) return W4A16_EINVAL;
     if (q.decode) {
         q.d = decode_geometry(M, 2 * ((N + 127) / 128 * 128), K, g, bits);

@@ -153,7 +153,9 @@ struct UnitWalk {
     }
 };
 
-// Tensor maps of a launch (GATED: P, S, Z of the gate projection, P2, S2, Z2 of the up one).
+// Tensor maps of a launch (GATED: P, S, Z of the gate projection, P2, S2, Z2 of the up one),
+// and the arguments that only GATED has.  (In DecodeArgs they changed the registers and the
+// schedule of the instances that do not use them: 70B-shaped layers 4% slower.)
 template <bool GATED>
 struct DecodeMaps {
     CUtensorMap P, X, S, Z;
@@ -161,17 +163,17 @@ struct DecodeMaps {
 template <>
 struct DecodeMaps<true> {
     CUtensorMap P, X, S, Z, P2, S2, Z2;
+    const uint16_t* scales2;     // the up projection's
+    const uint16_t* zeros2;
+    uint16_t* G;                 // the projections' outputs, or null
+    uint16_t* U;
+    int act;                     // w4a16_act
 };
 
 struct DecodeArgs {
     const uint16_t* scales;
     const uint16_t* zeros;
-    const uint16_t* scales2;     // GATED: the up projection's
-    const uint16_t* zeros2;
     uint16_t* Y;                 // GATED: H
-    uint16_t* G;                 // GATED: the projections' outputs, or null
-    uint16_t* U;
-    int act;                     // GATED: w4a16_act
     const uint16_t* act_scale;   // bf16 [K] per-input-channel activation scale, or null
     uint32_t* ws_flag;    // [(RB + C) slots][16 warps] ready flags
     float* ws_part;       // [(RB + C) slots][16 warps][32 lanes][4·MB] fp32 parts
@@ -254,8 +256,10 @@ __device__ __forceinline__ int unit_feature(int rb, int r) {
 }
 
 template <bool GATED>
-__device__ __forceinline__ const uint16_t* scale_base(const DecodeArgs& a, int arr, int r) {
-    if (GATED && r >= kDecRows / 2) return arr == 0 ? a.scales2 : a.zeros2;
+__device__ __forceinline__ const uint16_t* scale_base(const DecodeMaps<GATED>& maps, const DecodeArgs& a, int arr,
+                                                      int r) {
+    if constexpr (GATED)
+        if (r >= kDecRows / 2) return arr == 0 ? maps.scales2 : maps.zeros2;
     return arr == 0 ? a.scales : a.zeros;
 }
 
@@ -263,13 +267,13 @@ __device__ __forceinline__ const uint16_t* scale_base(const DecodeArgs& a, int a
 // are not 16-byte aligned: per array and row, GU·2 bytes as copies of CS bytes,
 // lane l taking rows l, l + 32, ... (no integer division in the loop).
 template <int GU, int CS, bool GATED>
-__device__ __forceinline__ void copy_scale_rows(const DecodeArgs& a, uint32_t sz, int sz_array, int rb,
-                                                int g0, int arrays, int lane) {
+__device__ __forceinline__ void copy_scale_rows(const DecodeMaps<GATED>& maps, const DecodeArgs& a, uint32_t sz,
+                                                int sz_array, int rb, int g0, int arrays, int lane) {
     constexpr int kPerRow = (GU * 2 + CS - 1) / CS;
     for (int arr = 0; arr < arrays; ++arr) {
 #pragma unroll 1
         for (int r = lane; r < kDecRows; r += 32) {
-            const uint16_t* base = scale_base<GATED>(a, arr, r);
+            const uint16_t* base = scale_base<GATED>(maps, a, arr, r);
             const int n = unit_feature<GATED>(rb, r);
             const uint32_t dst = sz + arr * sz_array + r * GU * 2;
 #pragma unroll
@@ -305,8 +309,8 @@ __device__ __forceinline__ void decode_store_y(const DecodeArgs& a, const float 
 // tokens 8mb + 2q and + 1.  H is rounded once, from the binary32 sums; G and U, when
 // they are kept for a backward pass, are rounded apart.
 template <int MB>
-__device__ __forceinline__ void decode_store_gated(const DecodeArgs& a, const float (&d)[MB][4], int rb,
-                                                   int w, int g, int q) {
+__device__ __forceinline__ void decode_store_gated(const DecodeMaps<true>& maps, const DecodeArgs& a,
+                                                   const float (&d)[MB][4], int rb, int w, int g, int q) {
     const int n = rb * (kDecRows / 2) + 8 * w + g;
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
@@ -315,10 +319,10 @@ __device__ __forceinline__ void decode_store_gated(const DecodeArgs& a, const fl
             const int m = 8 * mb + 2 * q + j;
             if (m < a.M && n < a.N) {
                 const int64_t at = (int64_t)m * a.N + n;
-                a.Y[at] = (uint16_t)f32_to_bf16_bits_rn(act_value(a.act, d[mb][j]) * d[mb][2 + j]);
-                if (a.G != nullptr) {
-                    a.G[at] = (uint16_t)f32_to_bf16_bits_rn(d[mb][j]);
-                    a.U[at] = (uint16_t)f32_to_bf16_bits_rn(d[mb][2 + j]);
+                a.Y[at] = (uint16_t)f32_to_bf16_bits_rn(act_value(maps.act, d[mb][j]) * d[mb][2 + j]);
+                if (maps.G != nullptr) {
+                    maps.G[at] = (uint16_t)f32_to_bf16_bits_rn(d[mb][j]);
+                    maps.U[at] = (uint16_t)f32_to_bf16_bits_rn(d[mb][2 + j]);
                 }
             }
         }
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     const int arr = e / (kDecRows / 8), j = e % (kDecRows / 8);
                     const int n = unit_feature<GATED>(rb, 8 * j);
                     const int valid = min(max(a.N - n, 0), 8);
-                    const uint16_t* src = scale_base<GATED>(a, arr, 8 * j) + (valid > 0 ? n : 0);
+                    const uint16_t* src = scale_base<GATED>(maps, a, arr, 8 * j) + (valid > 0 ? n : 0);
                     cp_async_16(sz + arr * kSzArray + 16 * j, src, 2u * (uint32_t)valid);
                 }
                 cp_async_arrive_noinc(bar);
@@ -498,12 +502,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                     // of cs, so a copy never straddles the end of a scale row
                     // (the host picks cs ≤ GU·2; instances with larger copies are never built)
                     if constexpr (GU * 2 >= 16) {
-                        if (cs == 16) copy_scale_rows<GU, 16, GATED>(a, sz, kSzArray, rb, g0, arrays, lane);
+                        if (cs == 16) copy_scale_rows<GU, 16, GATED>(maps, a, sz, kSzArray, rb, g0, arrays, lane);
                     }
                     if constexpr (GU * 2 >= 8) {
-                        if (cs == 8) copy_scale_rows<GU, 8, GATED>(a, sz, kSzArray, rb, g0, arrays, lane);
+                        if (cs == 8) copy_scale_rows<GU, 8, GATED>(maps, a, sz, kSzArray, rb, g0, arrays, lane);
                     }
-                    if (cs == 4) copy_scale_rows<GU, 4, GATED>(a, sz, kSzArray, rb, g0, arrays, lane);
+                    if (cs == 4) copy_scale_rows<GU, 4, GATED>(maps, a, sz, kSzArray, rb, g0, arrays, lane);
                     cp_async_arrive_noinc(bar);
                 } else if (cs == 3) {
                     // one group per unit (8-bit codes at g = 128) and an even number of
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                         for (int arr = 0; arr < arrays; ++arr) {
 #pragma unroll 4
                             for (int r = lane; r < kDecRows; r += 32) {
-                                const uint16_t* base = scale_base<GATED>(a, arr, r);
+                                const uint16_t* base = scale_base<GATED>(maps, a, arr, r);
                                 const int n = unit_feature<GATED>(rb, r);
                                 const bool in = n < a.N && gp < a.Gtot;
                                 cp_async_4(sz + arr * kSzArray + r * 4, base + (in ? (int64_t)n * a.Gtot + gp : 0),
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                                 const int rem = e - arr * (kDecRows * GU);
                                 const int r = rem / GU, j = rem - r * GU;
                                 const int n = unit_feature<GATED>(rb, r);
-                                const uint16_t* src = scale_base<GATED>(a, arr, r);
+                                const uint16_t* src = scale_base<GATED>(maps, a, arr, r);
                                 if (n < a.N && g0 + j < a.Gtot) v[t] = ldg_u16(src + (int64_t)n * a.Gtot + g0 + j);
                             }
                         }
@@ -937,7 +941,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         const int64_t first_u = (int64_t)rb * a.KBn;
         const bool whole = first_u >= u0 && first_u + a.KBn <= u1;
         if (whole) {
-            if constexpr (GATED) decode_store_gated<MB>(a, d, rb, w, g, q);
+            if constexpr (GATED) decode_store_gated<MB>(maps, a, d, rb, w, g, q);
             else decode_store_y<MB>(a, d, rb, w, g, q);
             continue;
         }
@@ -991,7 +995,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (lane == 0)                                        // consumed: the slots are free again
             for (int64_t p = c_first + 1; p <= c_last; ++p)
                 st_relaxed_u32(a.ws_flag + (rb + p) * kDecConsumers + w, 0u);
-        if constexpr (GATED) decode_store_gated<MB>(a, d, rb, w, g, q);
+        if constexpr (GATED) decode_store_gated<MB>(maps, a, d, rb, w, g, q);
         else decode_store_y<MB>(a, d, rb, w, g, q);
     }
 }

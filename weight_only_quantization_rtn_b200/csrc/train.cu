@@ -363,12 +363,12 @@ w4a16_status launch_gated_decode(const GatedPlan& q, const void* X, int64_t M, i
     DecodeArgs a{};
     a.scales = static_cast<const uint16_t*>(w[0].scales);
     a.zeros = static_cast<const uint16_t*>(w[0].zeros);
-    a.scales2 = static_cast<const uint16_t*>(w[1].scales);
-    a.zeros2 = static_cast<const uint16_t*>(w[1].zeros);
+    maps.scales2 = static_cast<const uint16_t*>(w[1].scales);
+    maps.zeros2 = static_cast<const uint16_t*>(w[1].zeros);
     a.Y = static_cast<uint16_t*>(H);
-    a.G = static_cast<uint16_t*>(G);
-    a.U = static_cast<uint16_t*>(U);
-    a.act = act;
+    maps.G = static_cast<uint16_t*>(G);
+    maps.U = static_cast<uint16_t*>(U);
+    maps.act = act;
     a.ws_flag = static_cast<uint32_t*>(workspace);
     a.ws_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + decode_flag_bytes(d, q.grid));
     a.M = (int)M;

@@ -6,7 +6,8 @@
 // in binary32 from the kept bf16 G and U, each rounded to bf16 once: they are results
 // (the gradients at the two projections' outputs, which adapters and weight gradients
 // start from) and the operands of the tensor-core product that gives dX, which takes
-// bf16.  Bound by memory: 10 bytes per element.  It is a pass of its own because
+// bf16.  Bound by memory: 10 bytes per element (2048 x 11008: 32 us, 7 TB/s with what L2
+// still holds).  It is a pass of its own because
 // the product reads each element once per block of 256 or 512 input channels: formed
 // inside it, the exponentials and three reads would be repeated as often.
 #pragma once

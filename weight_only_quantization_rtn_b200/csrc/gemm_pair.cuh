@@ -261,12 +261,27 @@ struct PairConfig {
 // Most tokens of a tile of one CTA: its token ring must hold a block for each A buffer.
 constexpr int kPairMaxSingle = 96;
 
-// A slots, code units and token blocks that the rings hold.  The latter two cover at least as
-// many blocks as there are A slots, so that a free A slot implies that what their slots held
-// before was used: a warp that awaits a slot's next phase cannot be looking at an older one.
+// A slots, code units and token blocks that the rings hold.
+//
+// A barrier's wait tells two successive phases apart, no more: a warp that awaits a slot's
+// next phase has to know that the phase before it has completed.  Blocks are numbered
+// through all segments of a CTA's share, group k dequantizes the blocks ≡ k modulo the number
+// of groups (pair_first), and a group waits for the A slot of its block first.
+//   A slot of block j, freed by the MMAs of block j − NA: those of block j − 2·NA are complete,
+//     because the group's last block, at most NA before this one, waited for no older ones.
+//   Code unit and tokens of block j: what their slots held before was loaded, because all
+//     blocks up to j − NA are multiplied and the rings cover at least NA blocks.
 struct PairRings {
     int na, sp, sx;
 };
+
+// First block of group `grp` in a segment, counted from the segment's first, which `before`
+// blocks of the share precede.
+__host__ __device__ inline int pair_first(int before, int grp, int groups) {
+    const int d = grp - before % groups;
+    return d < 0 ? d + groups : d;
+}
+
 template <typename Cfg>
 __host__ __device__ inline PairRings pair_rings(int bt, int acc_cols) {
     const int x_bytes = bt * kPairBlock * 2;
@@ -322,17 +337,17 @@ template <int UB>
 struct PairWalk {
     int tile, u0, units;
     int at, end;                 // split: this share's units still to do
-    __device__ __forceinline__ static int upt(const PairArgs& a) { return (a.blocks + UB - 1) / UB; }
+    __host__ __device__ __forceinline__ static int upt(const PairArgs& a) { return (a.blocks + UB - 1) / UB; }
     // First unit of a slot's share.
-    __device__ __forceinline__ static int start(const PairArgs& a, int c, int slots) {
+    __host__ __device__ __forceinline__ static int start(const PairArgs& a, int c, int slots) {
         return (int)((int64_t)a.tiles * upt(a) * c / slots);
     }
-    __device__ __forceinline__ void init(const PairArgs& a, int slot, int slots) {
+    __host__ __device__ __forceinline__ void init(const PairArgs& a, int slot, int slots) {
         tile = slot - slots;
         at = a.split ? start(a, slot, slots) : 0;
         end = a.split ? start(a, slot + 1, slots) : 0;
     }
-    __device__ __forceinline__ bool next(const PairArgs& a, int slots) {
+    __host__ __device__ __forceinline__ bool next(const PairArgs& a, int slots) {
         const int per = upt(a);
         if (!a.split) {
             tile += slots;
@@ -343,14 +358,16 @@ struct PairWalk {
         if (at >= end) return false;
         tile = at / per;
         u0 = at - tile * per;
-        units = min(end - at, per - u0);
+        units = end - at < per - u0 ? end - at : per - u0;
         at += units;
         return true;
     }
-    __device__ __forceinline__ int first_block() const { return u0 * UB; }
-    __device__ __forceinline__ int count(const PairArgs& a) const { return min((u0 + units) * UB, a.blocks) - u0 * UB; }
+    __host__ __device__ __forceinline__ int first_block() const { return u0 * UB; }
+    __host__ __device__ __forceinline__ int count(const PairArgs& a) const {
+        return ((u0 + units) * UB < a.blocks ? (u0 + units) * UB : a.blocks) - u0 * UB;
+    }
     // Slots [slot + 1, followers_end) hold the rest of the tile that this share begins.
-    __device__ __forceinline__ int followers_end(const PairArgs& a, int slot, int slots) const {
+    __host__ __device__ __forceinline__ int followers_end(const PairArgs& a, int slot, int slots) const {
         const int per = upt(a);
         int c = slot + 1;
         if (u0 == 0 && units < per)
@@ -992,10 +1009,12 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
             if (!more && !pending) break;
             const int nb = more ? walk.count(a) : 0, b0 = more ? walk.first_block() : 0;
             const int r0 = more ? pair_row0<DGRAD>(a, walk.tile, kCtas) : 0;
-            // this group's first block in each ring: slot and phase
-            int ab = (cnt + grp) % NA, xslot = (cnt + grp) % SX;
-            uint32_t aph = (uint32_t)((cnt + grp) / NA) & 1u, xph = (uint32_t)((cnt + grp) / SX) & 1u;
-            const int ufirst = ucnt + grp / UB;
+            // this group's first block of the segment (the turns go on from segment to segment: see
+            // PairRings), and its slot and phase in each ring
+            int i = pair_first(cnt, grp, NG);
+            int ab = (cnt + i) % NA, xslot = (cnt + i) % SX;
+            uint32_t aph = (uint32_t)((cnt + i) / NA) & 1u, xph = (uint32_t)((cnt + i) / SX) & 1u;
+            const int ufirst = ucnt + i / UB;
             int pslot = ufirst % SP;
             uint32_t pph = (uint32_t)(ufirst / SP) & 1u;
             cnt += nb;
@@ -1003,7 +1022,6 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
             // The A tiles of a block are written: visible to the tensor core, then counted; the
             // codes were used, so their slot is given back.  (Given back right behind the
             // loads, a slot was seen refilled before a load of it had been performed.)
-            int i = grp;
             auto release = [&]() {
                 if constexpr (Cfg::kTmemA) {
                     tmem_wait_st();
@@ -1164,8 +1182,8 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
 #pragma unroll
                 for (int t = 0; t < 4; ++t) sa[t] = za[t] = sn[t] = zn[t] = 0u;
                 if (more) {
-                    fetch(grp, sa, za);
-                    fetch(grp + NG, sn, zn);
+                    fetch(i, sa, za);
+                    fetch(i + NG, sn, zn);
                 }
                 const uint32_t row = ps + (uint32_t)(r * 128 + (BITS == 8 ? q * (kPairBlock * 128) : 0));
                 const uint32_t line = as + (uint32_t)(q * (kPairABytes / 2) + r * 128 + (((4 * q) ^ (r & 7)) * 16));

@@ -8,6 +8,7 @@
 //   must be found at fault.
 #include <cstdio>
 #include <cstdlib>
+#include <set>
 
 #include "../weight_only_quantization_rtn_b200/csrc/pair_plan.cuh"
 
@@ -31,7 +32,7 @@ static void check(int64_t M, int64_t rows, int64_t blocks, int sms) {
     PairArgs a{};
     pair_plan_args(p, &a);
     a.products = 1;
-    const PairRings r = pair_rings<Cfg>(a.bt, a.acc_cols);
+    const PairRings r = pair_rings<Cfg>(a.bt, a.acc_cols, a.blocks);
     // steps that the kernel takes without a modulus, ring sizes, shared memory, tensor memory
     if (NG > r.na || NG > r.sx || (UB - 1 + NG) / UB > r.sp || r.na > kPairMaxA || r.sp > kPairMaxX || r.sx > kPairMaxX ||
         r.sp * Cfg::kUnitBytes + r.sx * a.bt * kPairBlock * 2 > Cfg::kLoads ||
@@ -41,26 +42,40 @@ static void check(int64_t M, int64_t rows, int64_t blocks, int sms) {
     for (int slot = 0; slot < p.grid; ++slot) {
         PairWalk<UB> w;
         w.init(a, slot, p.grid);
-        int cnt = 0;
+        int cnt = 0, units = 0;
         int last[NG];                                  // each group's last block, -1: none
+        int unit_of[4096], first_of[4096];             // unit of a block; first block of a unit (of the last ones)
         for (int& l : last) l = -1;
+        std::set<int> own[NG];                         // blocks that a group dequantized
         while (w.next(a, p.grid)) {
             const int nb = w.count(a);
             covered += w.units;
+            for (int i = 0; i < nb; ++i) unit_of[(cnt + i) % 4096] = units + i / UB;
+            for (int u = 0; u < w.units; ++u) first_of[(units + u) % 4096] = cnt + u * UB;
             for (int i = 0; i < nb; ++i) {
-                const int j = cnt + i;
+                const int j = cnt + i, u = unit_of[j % 4096];
                 const int grp = g_restart ? i % NG : j % NG;
                 if (!g_restart && pair_first(cnt, grp, NG) % NG != i % NG) std::abort();
-                g_waits += 2;
+                g_waits += 3;
                 const int done = j - r.na;             // its MMAs are complete once the A slot is free
                 // A slot: the MMAs of block j - 2·NA
                 if (j >= 2 * r.na && last[grp] - r.na < j - 2 * r.na) fault("A slot", M, rows, blocks, sms, j);
+                // code unit: a block of the unit that held the slot before was dequantized
+                if (u >= r.sp) {
+                    const int f = first_of[(u - r.sp) % 4096];
+                    bool known = f <= done;
+                    for (int b : own[grp]) known = known || (b >= f && unit_of[b % 4096] == u - r.sp);
+                    if (!known) fault("code unit", M, rows, blocks, sms, j);
+                }
                 // tokens: block j - SX was multiplied
                 if (j >= r.sx && j - r.sx > done) fault("tokens", M, rows, blocks, sms, j);
                 last[grp] = j;
+                own[grp].insert(j);
+                if (own[grp].size() > 16) own[grp].erase(own[grp].begin());
             }
             cnt += nb;
-            if (cnt > 3000) break;                     // (steady by then)
+            units += w.units;
+            if (cnt > 3000) break;                     // (the tables above; steady by then)
         }
         if (cnt > 3000) covered = -1;
         if (covered < 0) break;

@@ -45,6 +45,14 @@ def test_whole_tiles(M, N, K, g, bits):
     gated_repeated(M, N, K, g, bits)
 
 
+# tiles of one, two and three blocks
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("M,path", [(3, "tensorcore"), (16, "tensorcore"), (20, "auto"), (40, "auto"), (64, "auto"), (90, "auto")])
+@pytest.mark.parametrize("K", [32, 64, 96, 160])
+def test_short_tiles(M, path, K, bits):
+    gated_repeated(M, 60000, K, 32, bits, path)
+
+
 # tiles shared by CTAs whose shares do not begin with a tile
 @pytest.mark.parametrize("bits,M,N,K", [(8, 80, 11008, 4096), (4, 80, 11008, 4096), (8, 61, 11008, 4096), (8, 96, 4096, 8192),
                                         (4, 96, 11008, 4160), (4, 61, 5000, 4032)])

@@ -270,10 +270,17 @@ constexpr int kPairMaxSingle = 96;
 //   A slot of block j, freed by the MMAs of block j − NA: those of block j − 2·NA are complete,
 //     because the group's last block, at most NA before this one, waited for no older ones.
 //   Code unit and tokens of block j: what their slots held before was loaded, because all
-//     blocks up to j − NA are multiplied and the rings cover at least NA blocks.
+//     blocks up to j − NA are multiplied and the rings cover at least NA blocks
+//     (a unit that ends a tile may hold as little as one block: `cover` below).
 struct PairRings {
     int na, sp, sx;
 };
+
+// Fewest blocks that `units` consecutive code units of `per_unit` blocks hold, when a tile has
+// `blocks` (units do not cross tiles, so a tile's last may be short).
+__host__ __device__ inline int pair_cover(int units, int per_unit, int blocks) {
+    return blocks <= per_unit ? units * blocks : units / 2 * (per_unit + 1) + units % 2;
+}
 
 // First block of group `grp` in a segment, counted from the segment's first, which `before`
 // blocks of the share precede.
@@ -283,7 +290,7 @@ __host__ __device__ inline int pair_first(int before, int grp, int groups) {
 }
 
 template <typename Cfg>
-__host__ __device__ inline PairRings pair_rings(int bt, int acc_cols) {
+__host__ __device__ inline PairRings pair_rings(int bt, int acc_cols, int blocks) {
     const int x_bytes = bt * kPairBlock * 2;
     PairRings r;
     if (Cfg::kTmemA) {
@@ -292,6 +299,8 @@ __host__ __device__ inline PairRings pair_rings(int bt, int acc_cols) {
         r.sx = (Cfg::kLoads - 4 * Cfg::kUnitBytes) / x_bytes;
         if (r.sx > kPairMaxX) r.sx = kPairMaxX;
         r.sp = (Cfg::kLoads - r.sx * x_bytes) / Cfg::kUnitBytes;
+        const int cover = pair_cover(r.sp, Cfg::kUnitBlocks, blocks);
+        if (r.na > cover) r.na = cover;              // (tiles of a single block)
     } else {
         r.na = Cfg::kGroups + 1;
         // tokens come from L2 and need less of a lead than codes do
@@ -720,7 +729,7 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    const PairRings rings = pair_rings<Cfg>(a.bt, a.acc_cols);
+    const PairRings rings = pair_rings<Cfg>(a.bt, a.acc_cols, a.blocks);
     const int NA = rings.na, SP = rings.sp, SX = rings.sx, x_bytes = a.bt * kPairBlock * 2;
     const uint32_t as = smem_u32(smem);              // NA x kPairABytes (not with kTmemA)
     const uint32_t ps = as + Cfg::kSmemA;            // SP code units

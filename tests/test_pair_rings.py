@@ -27,3 +27,11 @@ def test_walk_finds_turns_that_start_anew(walk):
     """Groups that begin every segment with their own k-th block may wait a ring's length too far."""
     r = subprocess.run([walk, "1"], capture_output=True, text=True)
     assert r.returncode == 1 and "A slot" in r.stdout, r.stdout
+
+
+def test_decode_first_owners_wait_for_earlier_blocks(tmp_path):
+    exe = tmp_path / "decode_shares"
+    subprocess.check_call([w4build.nvcc(), *w4build.ARCH, "-O2", "-std=c++17", "--expt-relaxed-constexpr", "-o", str(exe),
+                           os.path.join(HERE, "decode_shares.cu")])
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout

@@ -51,12 +51,12 @@
 //    permuted X to match.  Two accumulator sets break the MMA dependency chain.
 //  * A row block owned entirely by one CTA is rounded and written to Y by each
 //    warp for its 16 rows.  A row block that the stream-K partition splits
-//    between CTAs c_first .. c_last: every owner but c_first writes its fp32
+//    between shares c_first .. c_last (decode_share): every owner but c_first writes its fp32
 //    part (per warp, in fragment layout) to the workspace and then a ready flag;
 //    c_first — which reaches its part of that row block last, because every CTA
 //    visits the row block it shares with its predecessor first and the one it
 //    shares with its successor second — waits for the flags (bounded), adds the
-//    parts to its own in CTA order and writes Y.  The sum order is fixed, so the
+//    parts to its own in the shares' order and writes Y.  The sum order is fixed, so the
 //    result is deterministic, and no second kernel is launched.
 //  * Programmatic dependent launch lets the next kernel on the stream start
 //    while this one drains; nothing but those static weights is read, and
@@ -105,9 +105,14 @@ constexpr uint32_t kDecProducerSleepNs = 256;
 constexpr uint32_t kDecHelperSleepNs = 128;
 
 // Unit u -> CTA that owns it under the even split u_c = floor(c·U/C).
-__device__ __forceinline__ int64_t owner_of(int64_t u, int64_t U, int64_t C) {
+__host__ __device__ __forceinline__ int64_t owner_of(int64_t u, int64_t U, int64_t C) {
     return ((u + 1) * C - 1) / U;
 }
+
+// Share of a block of the grid.  Shares are numbered from the last block to the first: the first
+// owner of a row block waits for the shares behind its own, so for blocks of lower index,
+// which are on the machine before it, and every wait ends however few SMs other work leaves.
+__host__ __device__ __forceinline__ uint32_t decode_share(uint32_t block, uint32_t C) { return C - 1u - block; }
 
 // Order in which a CTA visits its units [u0, u1): the partial row block at the
 // start of the range (shared with the previous CTA, which finishes that row
@@ -390,7 +395,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int64_t C = gridDim.x;
-    const int64_t cta = blockIdx.x;
+    // (opaque: folded into the arithmetic on the units, the subtraction changed the schedule of the
+    // main loop, and the linear layer's 28672 x 8192, M = 8, took 42.3 us instead of 40.3)
+    const int64_t cta = opaque_u32(decode_share(blockIdx.x, gridDim.x));
     const int64_t u0 = cta * a.units / C;
     const int64_t u1 = (cta + 1) * a.units / C;
     const int nunits = (int)(u1 - u0);
@@ -963,7 +970,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         // first owner: wait until every other owner has published (each lane
         // acquires the flags itself, so its reads of the parts follow them), load
         // the parts eight at a time, four with two column blocks (one round trip
-        // for most row blocks), and add them in CTA order, then write Y
+        // for most row blocks), and add them in order, then write Y
         bool ok = true;
         for (int64_t p = c_first + 1; p <= c_last && ok; ++p)
             ok = wait_flag(a.ws_flag + (rb + p) * kDecConsumers + w);

@@ -364,7 +364,10 @@ w4a16_status w8a8_gemm(const void* qx, const void* sx, int64_t M, int64_t K, con
  * Scales are below 2^122 (those of weights up to about 2^125 are).
  * Every product is accumulated in binary32.  Results are deterministic.  Every
  * workspace is scratch: calls that may run at the same time (two streams, two
- * captured graphs) need two.
+ * captured graphs) need two.  A call that follows one that gave up a wait
+ * (W4A16_DEVERR_WAIT) needs nothing done to the workspace; a captured graph that
+ * holds such a call needs its workspace set to zero, or to be captured again, before
+ * it is replayed.
  * ------------------------------------------------------------------------- */
 
 /* Activations of the gated block. */

@@ -1,8 +1,10 @@
 // Host-side check of the decode kernel's split, built and run by test_pair_rings.py: every row
 // block's first owner waits only for blocks of the grid with a lower index than its own.
+// And that no two launches have one value for the ready flags of their workspaces.
 #include <cstdio>
+#include <set>
 
-#include "../weight_only_quantization_rtn_b200/csrc/gemv_decode.cuh"
+#include "../weight_only_quantization_rtn_b200/csrc/host.cuh"
 
 using namespace w4a16;
 
@@ -28,6 +30,9 @@ int main() {
                             return std::printf("block %ld waits for block %ld\n", (long)block_of[first], (long)block_of[p]), 1;
                 }
             }
+    std::set<uint64_t> flags;
+    for (int i = 0; i < 200000; ++i) flags.insert(launch_flag());
+    if (flags.size() != 200000 || flags.count(0)) return std::printf("ready flags repeat\n"), 1;
     std::printf("%ld waits\n", waits);
     return waits == 0;
 }

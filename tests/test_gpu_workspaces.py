@@ -1,0 +1,44 @@
+"""Workspaces that hold what earlier calls may have left there: anything at all, ready flags of
+other launches included."""
+import pytest
+import torch
+
+import workloads
+import weight_only_quantization_rtn_b200 as w4
+from weight_only_quantization_rtn_b200 import build as w4build
+from test_gpu_train_paths import random_weights
+
+pytestmark = pytest.mark.gpu
+
+# 64-bit words: nothing, all ones, and the values that marked a part ready in every launch
+WORDS = [0, -1, 0x9E6C63D07F8A5C3D - (1 << 64), 0x7F8A5C3D7F8A5C3D]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    w4build.build()
+    yield
+    assert w4.device_error() == 0
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+@pytest.mark.parametrize("M", [20, 77, 200])
+@pytest.mark.parametrize("word", WORDS)
+def test_shared_tiles_of_the_gradient(M, word):
+    N, K, g = 4096, 512, 128
+    w = random_weights(N, K, g, 4, 3)
+    dY = workloads.make_activation(M, N, 4).cuda()
+    want = w4.gemm_dgrad(dY, *w, g=g)
+    L = w4.lib()
+    nbytes = L.w4a16_gemm_dgrad_workspace_size(M, N, K, g)
+    assert nbytes > 0                                         # tiles are shared
+    ws = torch.full((nbytes // 8,), word, dtype=torch.int64, device="cuda")
+    dX = torch.empty_like(want)
+    for _ in range(3):
+        assert L.w4a16_gemm_dgrad(dY.data_ptr(), M, N, *(t.data_ptr() for t in w), K, g, 0, dX.data_ptr(), ws.data_ptr(),
+                                  nbytes, stream()) == 0
+        assert torch.equal(dX, want)
+        ws.fill_(word)

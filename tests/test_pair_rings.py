@@ -29,7 +29,7 @@ def test_walk_finds_turns_that_start_anew(walk):
     assert r.returncode == 1 and "A slot" in r.stdout, r.stdout
 
 
-def test_decode_first_owners_wait_for_earlier_blocks(tmp_path):
+def test_decode_shares_and_ready_flags(tmp_path):
     exe = tmp_path / "decode_shares"
     subprocess.check_call([w4build.nvcc(), *w4build.ARCH, "-O2", "-std=c++17", "--expt-relaxed-constexpr", "-o", str(exe),
                            os.path.join(HERE, "decode_shares.cu")])

@@ -334,11 +334,13 @@ struct PairArgs {
     int tiles;
     int split;                   // 1: the tiles' code units are divided evenly over the CTAs
     uint64_t* flags;             // [slots][CTAs of a slot][kPairMaxWarps] ready flags of the parts
+    uint64_t ready;              // the flags' value in this launch
 };
 
-// Ready flag of a part: no sum, index or bf16 data is likely to hold it, so the workspace
-// needs no clearing before its first use; the first owner clears a flag that it consumed.
-constexpr uint64_t kPairFlagReady = 0x9E6C63D07F8A5C3Dull;
+// Ready flag of a part: the launch's own 64-bit value (launch_flag), which neither data nor a
+// flag that an earlier launch left behind holds, so the workspace needs no clearing before its
+// first use.  The first owner clears a flag that it consumed: a captured launch, which keeps its
+// value, finds its flags clear.
 
 // A CTA's (pair's) share of the work, as segments (tile, first unit, units).  The host
 // refuses problems of 2^31 units and more.
@@ -396,10 +398,10 @@ __device__ __forceinline__ void st_release_u64(uint64_t* p, uint64_t v) {
 }
 
 // Wait for another CTA's part (bounded: about one second).
-__device__ __forceinline__ bool pair_wait_flag(const uint64_t* flag) {
+__device__ __forceinline__ bool pair_wait_flag(const uint64_t* flag, uint64_t ready) {
     uint64_t t0 = 0;
     for (uint32_t tries = 1;; ++tries) {
-        if (ld_acquire_u64(flag) == kPairFlagReady) return true;
+        if (ld_acquire_u64(flag) == ready) return true;
         __nanosleep(100);
         if ((tries & 63u) == 0u) {
             const uint64_t now = global_timer_ns();
@@ -638,7 +640,7 @@ __device__ __forceinline__ bool pair_epilogue(const PairArgs& a, const PairTileD
     const uint32_t t_lane = t.tmem + ((uint32_t)(quarter * 32) << 16);
     const int64_t part_floats = pair_part_floats(mma_n);
     for (int c = t.slot + 1; c < t.followers_end && ok; ++c)
-        ok = pair_wait_flag(a.flags + ((int64_t)c * kCtas + rank) * kPairMaxWarps + w);
+        ok = pair_wait_flag(a.flags + ((int64_t)c * kCtas + rank) * kPairMaxWarps + w, a.ready);
     if (!__all_sync(0xffffffffu, ok ? 1 : 0)) return false;
     // strips of this warp: the quarter's strips are dealt over its warps
 #pragma unroll 1
@@ -708,7 +710,7 @@ __device__ __forceinline__ bool pair_epilogue(const PairArgs& a, const PairTileD
         __threadfence();                               // every lane's part before the flag
         __syncwarp();
         if (lane == 0)
-            st_release_u64(a.flags + ((int64_t)t.slot * kCtas + rank) * kPairMaxWarps + w, kPairFlagReady);
+            st_release_u64(a.flags + ((int64_t)t.slot * kCtas + rank) * kPairMaxWarps + w, a.ready);
     } else if (t.followers_end > t.slot + 1) {
         __syncwarp();
         if (lane == 0)                                 // the parts were read: their flags are free again

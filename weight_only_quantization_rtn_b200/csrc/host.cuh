@@ -78,6 +78,14 @@ inline w4a16_status encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
     return W4A16_OK;
 }
 
+// Value of the ready flags of one launch: another one for every launch of the process (the
+// multiplication by an odd number is one to one), never 0, and like no data.
+inline uint64_t launch_flag() {
+    static std::atomic<uint64_t> launches{1};
+    const uint64_t v = launches.fetch_add(1, std::memory_order_relaxed) * 0x9E3779B97F4A7C15ull;
+    return v != 0 ? v : 1;
+}
+
 inline w4a16_status launch_status() {
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? W4A16_OK : W4A16_ECUDA;

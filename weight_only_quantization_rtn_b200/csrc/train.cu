@@ -93,6 +93,7 @@ w4a16_status launch_pair_t(const PairPlan& p, const CUtensorMap* tmX, const CUte
     pair_plan_args(p, &args);
     if (p.split) {
         args.flags = static_cast<uint64_t*>(workspace);
+        args.ready = launch_flag();
         args.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.flag_bytes);
     }
     cudaLaunchAttribute attr[1];

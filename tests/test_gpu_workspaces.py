@@ -42,3 +42,25 @@ def test_shared_tiles_of_the_gradient(M, word):
                                   nbytes, stream()) == 0
         assert torch.equal(dX, want)
         ws.fill_(word)
+
+
+@pytest.mark.parametrize("bits,M", [(4, 1), (4, 8), (4, 16), (8, 5)])
+@pytest.mark.parametrize("word", WORDS)
+def test_shared_row_blocks_of_the_gated_block(M, bits, word):
+    N, K, g = 1000, 4096, 128
+    gate, up = random_weights(N, K, g, bits, 3), random_weights(N, K, g, bits, 4)
+    X = workloads.make_activation(M, K, 5).cuda()
+    f = w4.gated if bits == 4 else w4.gated8
+    want = f(X, gate, up, g=g, path="decode")
+    L = w4.lib()
+    size, call = ((L.w4a16_gated_workspace_size, L.w4a16_gated) if bits == 4 else
+                  (L.w8a16_gated_workspace_size, L.w8a16_gated))
+    nbytes = size(M, N, K, g, w4.PATH_DECODE)
+    assert nbytes > 0
+    ws = torch.full((nbytes // 8,), word, dtype=torch.int64, device="cuda")
+    H = torch.empty_like(want)
+    for _ in range(3):
+        assert call(X.data_ptr(), M, K, *(t.data_ptr() for t in gate), *(t.data_ptr() for t in up), N, g, 0, 0,
+                    H.data_ptr(), None, None, ws.data_ptr(), nbytes, w4.PATH_DECODE, stream()) == 0
+        assert torch.equal(H, want)
+        ws.fill_(word)

@@ -155,6 +155,17 @@ __device__ __forceinline__ void dequant8_natural(uint32_t w, uint32_t zz, uint32
     }
 }
 
+// ------------------------------------------------------------------ flags between CTAs
+__device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t* p) {
+    uint64_t v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_release_u64(uint64_t* p, uint64_t v) {
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+
 // ------------------------------------------------------------------ asynchronous copies
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes) {
     // 4-byte async copy global -> shared; bytes beyond src_bytes (0 or 4) are zero-filled.

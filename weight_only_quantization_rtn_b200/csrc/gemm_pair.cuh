@@ -387,16 +387,6 @@ struct PairWalk {
     }
 };
 
-__device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t* p) {
-    uint64_t v;
-    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-    return v;
-}
-
-__device__ __forceinline__ void st_release_u64(uint64_t* p, uint64_t v) {
-    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
-}
-
 // Wait for another CTA's part (bounded: about one second).
 __device__ __forceinline__ bool pair_wait_flag(const uint64_t* flag, uint64_t ready) {
     uint64_t t0 = 0;

@@ -98,6 +98,17 @@ constexpr int kDecSlabBytes = 2 * kDecSlabArrayBytes;   // scales and zeros
 // floating-point arithmetic produces, so stale partial sums are never mistaken
 // for it.
 constexpr uint32_t kDecFlagReady = 0x7F8A5C3Du;
+// GATED: 64-bit flags with a value of the launch's own (launch_flag): its workspace comes from an
+// allocator at every call and holds any data, codes or random bits, where 32 bits would meet
+// the pattern once in some 10^6 calls.
+template <bool GATED>
+struct DecodeFlag {
+    using type = uint32_t;
+};
+template <>
+struct DecodeFlag<true> {
+    using type = uint64_t;
+};
 // Longest sleep between polls of a waiting producer / helper: the ring holds
 // several microseconds of data, so a late wake-up costs nothing, while polling
 // in a tight loop would take issue slots from the consumer warps.
@@ -173,6 +184,7 @@ struct DecodeMaps<true> {
     const uint16_t* zeros2;
     uint16_t* G;                 // the projections' outputs, or null
     uint16_t* U;
+    uint64_t ready;              // the flags' value in this launch
     int act;                     // w4a16_act
 };
 
@@ -181,7 +193,7 @@ struct DecodeArgs {
     const uint16_t* zeros;
     uint16_t* Y;                 // GATED: H
     const uint16_t* act_scale;   // bf16 [K] per-input-channel activation scale, or null
-    uint32_t* ws_flag;    // [(RB + C) slots][16 warps] ready flags
+    void* ws_flag;        // [(RB + C) slots][16 warps] ready flags (DecodeFlag)
     float* ws_part;       // [(RB + C) slots][16 warps][32 lanes][4·MB] fp32 parts
     int M;
     int N;
@@ -226,8 +238,12 @@ __device__ __forceinline__ void st_release_u32(uint32_t* p, uint32_t v) {
     asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
-__device__ __forceinline__ void st_relaxed_u32(uint32_t* p, uint32_t v) {
+__device__ __forceinline__ void st_relaxed(uint32_t* p, uint32_t v) {
     asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void st_relaxed(uint64_t* p, uint64_t v) {
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
 
 __device__ __forceinline__ float4 ld_cg_f4(const float* p) {
@@ -241,12 +257,16 @@ __device__ __forceinline__ float4 ld_cg_f4(const float* p) {
 
 // Wait until another CTA has published its part (bounded: about one second,
 // then the error is recorded and false returned).
-__device__ __forceinline__ bool wait_flag(const uint32_t* flag) {
-    if (ld_acquire_u32(flag) == kDecFlagReady) return true;
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) { return ld_acquire_u32(p); }
+__device__ __forceinline__ uint64_t ld_acquire(const uint64_t* p) { return ld_acquire_u64(p); }
+
+template <typename F>
+__device__ __forceinline__ bool wait_flag(const F* flag, F ready) {
+    if (ld_acquire(flag) == ready) return true;
     const uint64_t t0 = global_timer_ns();
     while (true) {
         __nanosleep(64);
-        if (ld_acquire_u32(flag) == kDecFlagReady) return true;
+        if (ld_acquire(flag) == ready) return true;
         if (global_timer_ns() - t0 > kWaitTimeoutNs) {
             report_error(kErrMbarTimeout);
             return false;
@@ -955,6 +975,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         const int64_t c_first = owner_of(first_u, a.units, C);
         const int64_t c_last = owner_of(first_u + a.KBn - 1, a.units, C);
+        using Flag = typename DecodeFlag<GATED>::type;
+        Flag* const flags = static_cast<Flag*>(a.ws_flag);
+        Flag ready;
+        if constexpr (GATED) ready = maps.ready;
+        else ready = kDecFlagReady;
         if (cta != c_first) {
             // publish this CTA's part, then its ready flag
             const int64_t slot = rb + cta;
@@ -964,7 +989,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 *reinterpret_cast<float4*>(part + 4 * mb) = make_float4(d[mb][0], d[mb][1], d[mb][2], d[mb][3]);
             __threadfence();                                 // every lane's part, before the flag
             __syncwarp();
-            if (lane == 0) st_relaxed_u32(a.ws_flag + slot * kDecConsumers + w, kDecFlagReady);
+            if (lane == 0) st_relaxed(flags + slot * kDecConsumers + w, ready);
             continue;
         }
         // first owner: wait until every other owner has published (each lane
@@ -973,7 +998,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         // for most row blocks), and add them in order, then write Y
         bool ok = true;
         for (int64_t p = c_first + 1; p <= c_last && ok; ++p)
-            ok = wait_flag(a.ws_flag + (rb + p) * kDecConsumers + w);
+            ok = wait_flag(flags + (rb + p) * kDecConsumers + w, ready);
         if (!__all_sync(0xffffffffu, ok ? 1 : 0)) {
             *abort_flag = 1;
             continue;
@@ -1002,7 +1027,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         __syncwarp();
         if (lane == 0)                                        // consumed: the slots are free again
             for (int64_t p = c_first + 1; p <= c_last; ++p)
-                st_relaxed_u32(a.ws_flag + (rb + p) * kDecConsumers + w, 0u);
+                st_relaxed(flags + (rb + p) * kDecConsumers + w, Flag(0));
         if constexpr (GATED) decode_store_gated<MB>(maps, a, d, rb, w, g, q);
         else decode_store_y<MB>(a, d, rb, w, g, q);
     }

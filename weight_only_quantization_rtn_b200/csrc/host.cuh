@@ -198,15 +198,17 @@ inline bool decode_geometry_ok(const DecodeGeometry& d, int64_t M) {
 
 // Workspace of a decode launch with `ctas` CTAs: (rb + ctas) slots, slot rb + c
 // holding CTA c's part of a row block that the stream-K partition splits —
-// per slot 16 ready flags, then 16 warps x 32 lanes x 4·mb fp32 partial sums.
+// per slot 16 ready flags (DecodeFlag), then 16 warps x 32 lanes x 4·mb fp32 partial sums.
 // Scratch: no initialization is needed (a flag counts only when it holds the
 // ready pattern, which the consuming CTA clears again).
+template <typename Flag = uint32_t>
 inline int64_t decode_flag_bytes(const DecodeGeometry& d, int64_t ctas) {
-    return ((int64_t)(d.rb + ctas) * kDecConsumers * 4 + 255) / 256 * 256;
+    return ((int64_t)(d.rb + ctas) * kDecConsumers * (int64_t)sizeof(Flag) + 255) / 256 * 256;
 }
 
+template <typename Flag = uint32_t>
 inline int64_t decode_workspace_bytes(const DecodeGeometry& d, int64_t ctas) {
-    return decode_flag_bytes(d, ctas) + (int64_t)(d.rb + ctas) * kDecConsumers * 32 * 16 * d.mb;
+    return decode_flag_bytes<Flag>(d, ctas) + (int64_t)(d.rb + ctas) * kDecConsumers * 32 * 16 * d.mb;
 }
 
 // Row blocks the even unit split cuts between CTAs.

@@ -248,7 +248,7 @@ w4a16_status gated_plan(int64_t M, int64_t N, int64_t K, int32_t g, int32_t path
         q.grid = current_sm_count();
         if (q.grid > q.d.units) q.grid = q.d.units;
         if (q.grid < 1) q.grid = 1;
-        q.bytes = decode_workspace_bytes(q.d, q.grid);
+        q.bytes = decode_workspace_bytes<uint64_t>(q.d, q.grid);
     } else {
         q.p = pair_plan(M, N, kPairRows, (K + kPairBlock - 1) / kPairBlock, gated_unit_blocks(M, bits), current_sm_count());
         q.bytes = q.p.bytes;
@@ -294,8 +294,9 @@ w4a16_status launch_gated_decode(const GatedPlan& q, const void* X, int64_t M, i
     maps.G = static_cast<uint16_t*>(G);
     maps.U = static_cast<uint16_t*>(U);
     maps.act = act;
-    a.ws_flag = static_cast<uint32_t*>(workspace);
-    a.ws_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + decode_flag_bytes(d, q.grid));
+    maps.ready = launch_flag();
+    a.ws_flag = workspace;
+    a.ws_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + decode_flag_bytes<uint64_t>(d, q.grid));
     a.M = (int)M;
     a.N = (int)N;
     a.K = (int)K;

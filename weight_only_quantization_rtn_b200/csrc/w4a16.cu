@@ -199,7 +199,7 @@ w4a16_status launch_decode(const w4a16_plan& p, const void* X, int64_t M, int64_
     args.zeros = static_cast<const uint16_t*>(zeros);
     args.Y = static_cast<uint16_t*>(Y);
     args.act_scale = static_cast<const uint16_t*>(act_scale);
-    args.ws_flag = static_cast<uint32_t*>(workspace);
+    args.ws_flag = workspace;
     args.ws_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                             decode_flag_bytes(d, p.grid));
     args.M = (int)M;

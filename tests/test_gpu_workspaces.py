@@ -64,3 +64,25 @@ def test_shared_row_blocks_of_the_gated_block(M, bits, word):
                     H.data_ptr(), None, None, ws.data_ptr(), nbytes, w4.PATH_DECODE, stream()) == 0
         assert torch.equal(H, want)
         ws.fill_(word)
+
+
+@pytest.mark.parametrize("M,N", [(1500, 2048), (1500, 2047)])
+@pytest.mark.parametrize("swap", [False, True])
+def test_gate_gradient_over_its_inputs(M, N, swap):
+    """dG and dU in G's and U's memory (or the other way round), each thread going through many
+    elements, several calls in a row."""
+    K, g = 64, 32
+    w = random_weights(N, K, g, 4, 6)
+    dH, G0, U0 = (workloads.make_activation(M, N, s).cuda() for s in (1, 2, 3))
+    want = w4.gated_backward(dH, G0, U0, w, w, g=g)
+    L = w4.lib()
+    nbytes = L.w4a16_gated_backward_workspace_size(M, N, K, g)
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device="cuda")
+    ptrs = [t.data_ptr() for t in w]
+    for _ in range(4):
+        G, U = G0.clone(), U0.clone()
+        dG, dU = (U, G) if swap else (G, U)
+        dX = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+        assert L.w4a16_gated_backward(dH.data_ptr(), G.data_ptr(), U.data_ptr(), M, N, *ptrs, *ptrs, K, g, 0, 0,
+                                      dX.data_ptr(), dG.data_ptr(), dU.data_ptr(), ws.data_ptr(), nbytes, stream()) == 0
+        assert all(torch.equal(a, b) for a, b in zip(want, (dX, dG, dU)))

@@ -41,6 +41,16 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
     return v;
 }
 
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+    // The same from memory that the kernel may write too.
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 __device__ __forceinline__ uint4 ldg_cached(const void* p) {
     uint4 v;
     asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"

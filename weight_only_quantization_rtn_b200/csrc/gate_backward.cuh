@@ -23,15 +23,16 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     return r;
 }
 
+// dG and dU may be G's and U's own memory, so those four are not declared apart and G and U are
+// not read through the read-only path; each element is read and then written by one thread.
+//
 // Eight elements per thread and step over the flat arrays (16-byte chunks).
-__global__ void __launch_bounds__(256) gate_backward_kernel(const uint4* __restrict__ dH,
-                                                            const uint4* __restrict__ G,
-                                                            const uint4* __restrict__ U, int64_t chunks,
-                                                            int act, uint4* __restrict__ dG,
-                                                            uint4* __restrict__ dU) {
+__global__ void __launch_bounds__(256) gate_backward_kernel(const uint4* __restrict__ dH, const uint4* G,
+                                                            const uint4* U, int64_t chunks, int act, uint4* dG,
+                                                            uint4* dU) {
     for (int64_t c = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; c < chunks;
          c += (int64_t)gridDim.x * blockDim.x) {
-        const uint4 h = ldg_stream(dH + c), g = ldg_stream(G + c), u = ldg_stream(U + c);
+        const uint4 h = ldg_stream(dH + c), g = ld_stream(G + c), u = ld_stream(U + c);
         const uint32_t hv[4] = {h.x, h.y, h.z, h.w}, gv[4] = {g.x, g.y, g.z, g.w}, uv[4] = {u.x, u.y, u.z, u.w};
         uint32_t og[4], ou[4];
 #pragma unroll
@@ -58,11 +59,8 @@ __global__ void __launch_bounds__(256) gate_backward_kernel(const uint4* __restr
 // The same for rows of any length, element by element, with copies of dG and dU in rows
 // padded with zeros to `ld` elements (a multiple of 8: TMA rows start on 16 bytes).
 __global__ void __launch_bounds__(256) gate_backward_rows_kernel(const uint16_t* __restrict__ dH,
-                                                                 const uint16_t* __restrict__ G,
-                                                                 const uint16_t* __restrict__ U, int64_t M,
-                                                                 int N, int ld, int act,
-                                                                 uint16_t* __restrict__ dG,
-                                                                 uint16_t* __restrict__ dU,
+                                                                 const uint16_t* G, const uint16_t* U, int64_t M,
+                                                                 int N, int ld, int act, uint16_t* dG, uint16_t* dU,
                                                                  uint16_t* __restrict__ pG,
                                                                  uint16_t* __restrict__ pU) {
     const int64_t total = M * ld;

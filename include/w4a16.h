@@ -454,7 +454,7 @@ w4a16_status w4a16_gemm_wgrad(const void* dY, const void* X, int64_t M, int64_t 
 /* Embedding from a quantized table [V, K]: out[t, :] = bf16_rn(scale·Ŵ[ids[t], :]).
  *   ids in int32 or int64 [T] (id_bytes 4 or 8), aligned to id_bytes; out bf16 [T, K].
  * An id below 0 is padding and gives a row of zeros.  An id not below V gives a row of
- * zeros too and sets the device error word to W4A16_DEVERR_ID. */
+ * zeros too and sets W4A16_DEVERR_ID in the device error word. */
 w4a16_status w4a16_embedding(const void* ids, int32_t id_bytes, int64_t T, const void* packed,
                              const void* scales, const void* zeros, int64_t V, int64_t K,
                              int32_t g, int32_t sym, float scale, void* out, void* stream);
@@ -469,19 +469,20 @@ size_t w4a16_embedding_grad_workspace_size(int64_t T, int64_t V, int64_t K);
  * quantizer): dW[v, :] = scale·Σ_{t: ids[t] = v} dY[t, :], summed in binary32 over the
  * tokens sorted by id, in a fixed order; rows that no token names are written as zeros.
  *   dY bf16 [T, K], K a multiple of 32; ids as above; dW out [V, K], binary32 (f32 = 1) or bf16 (0).
- * Ids below 0 are padding and add nothing; so do ids not below V, which set the device
- * error word to W4A16_DEVERR_ID. */
+ * Ids below 0 are padding and add nothing; so do ids not below V, which set
+ * W4A16_DEVERR_ID in the device error word. */
 w4a16_status w4a16_embedding_grad(const void* dY, const void* ids, int32_t id_bytes, int64_t T,
                                   int64_t V, int64_t K, float scale, int32_t f32, void* dW,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
-/* Device error word: what a kernel reported. */
+/* Device error word: the kinds of report that kernels made, one bit each. */
 #define W4A16_DEVERR_WAIT 1   /* a bounded wait was given up */
 #define W4A16_DEVERR_ID 2     /* an embedding met an id not below the table's rows */
 
 /* Read and clear the current device's error word, written by a kernel that gave
  * up a bounded wait (a pipeline barrier that did not complete within about one
- * second) or met a bad id (W4A16_DEVERR_*).  *code = 0 when no kernel reported one.
+ * second) or met a bad id: W4A16_DEVERR_*, OR'ed when both happened.  *code = 0 when no
+ * kernel reported one.
  * Synchronizes the device. */
 w4a16_status w4a16_device_error(int32_t* code);
 

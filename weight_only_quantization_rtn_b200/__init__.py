@@ -582,8 +582,8 @@ def linear_w8a8(X: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,
 
 
 def device_error() -> int:
-    """Read and clear the device error word (0: nothing; 1: a kernel gave up a bounded
-    wait; 2: an embedding met an id not below its table's rows)."""
+    """Read and clear the device error word, a set of bits (0: nothing; 1: a kernel gave up a
+    bounded wait; 2: an embedding met an id not below its table's rows)."""
     code = ctypes.c_int32(0)
     _check(lib().w4a16_device_error(ctypes.byref(code)), "w4a16_device_error")
     return int(code.value)

@@ -29,7 +29,8 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
     return t;
 }
 
-__device__ __forceinline__ void report_error(int code) { atomicCAS(&g_device_error, 0, code); }
+// (the word is a set of bits: one kind of report does not hide another)
+__device__ __forceinline__ void report_error(int code) { atomicOr(&g_device_error, code); }
 
 // ------------------------------------------------------------------ loads
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {

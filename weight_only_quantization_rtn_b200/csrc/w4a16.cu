@@ -783,7 +783,7 @@ w4a16_status w4a16_device_error(int32_t* code) {
     if (cudaMemcpyToSymbol(g_device_error, &zero, sizeof(int)) != cudaSuccess) return W4A16_ECUDA;
     int other = 0;                      // the word of the other translation unit with kernels that report
     if (train_take_device_error(&other) != 0) return W4A16_ECUDA;
-    *code = value != 0 ? value : other;
+    *code = value | other;
     return W4A16_OK;
 }
 

@@ -133,7 +133,7 @@ __device__ __forceinline__ void zero_rows_by_ids(const void* ids, int wide, int6
             if (id[j] >= v0 && id[j] < v1) atomicOr(&mask[(id[j] - v0) >> 5], 1u << ((id[j] - v0) & 31));
     }
     __syncthreads();
-    const int row16 = K * (F32 ? 4 : 2) / 16;
+    const int row16 = K / (F32 ? 4 : 8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int64_t v = v0 + warp; v < v1; v += THREADS / 32) {
         if ((mask[(v - v0) >> 5] >> ((v - v0) & 31)) & 1u) continue;
@@ -380,7 +380,7 @@ __device__ __forceinline__ void zero_rows(const uint32_t* key, int64_t padded, i
     }
     __syncthreads();
     const uint32_t mask = *present;
-    const int row16 = K * (F32 ? 4 : 2) / 16;                   // K is a multiple of 32
+    const int row16 = K / (F32 ? 4 : 8);                        // K is a multiple of 32
     uint4* o = static_cast<uint4*>(dW) + v0 * row16;
     for (int r = 0; r < rows; ++r) {
         if ((mask >> r) & 1u) continue;

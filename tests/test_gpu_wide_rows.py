@@ -32,3 +32,40 @@ def test_embedding_grad(K, dtype):
             assert torch.equal(out[v], dY[0].to(dtype))
         else:
             assert int(out[v].count_nonzero()) == 0, v       # (a NaN is not zero)
+
+
+def wide_weights(N, K, g, bits, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randint(0, 256, (N, K * bits // 8), generator=gen, dtype=torch.uint8, device="cuda"),
+            (torch.rand(N, K // g, generator=gen, device="cuda") * 0.02 + 0.001).bfloat16(),
+            torch.randint(0, 1 << bits, (N, K // g), generator=gen, device="cuda").bfloat16())
+
+
+# codes that begin 2^31 bits into a row
+WIDE = [(4, (1 << 29) + 4096), (8, (1 << 28) + 4096)]
+
+
+@pytest.mark.parametrize("bits,K", WIDE)
+def test_gated(bits, K):
+    """One-hot tokens bring single weights out exactly."""
+    M, N, g = 17, 2, 128
+    gate, up = wide_weights(N, K, g, bits, 1), wide_weights(N, K, g, bits, 2)
+    X = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    at = [0, 77, K // 2, K - 1] + [K - 1 - 257 * i for i in range(1, 14)]
+    for m, k in enumerate(at):
+        X[m, k] = 1.0
+    f, dq = (w4.gated, w4.dequantize) if bits == 4 else (w4.gated8, w4.dequantize8)
+    _, G, U = f(X, gate, up, g=g, save=True)
+    del X
+    for Y, w in ((G, gate), (U, up)):
+        assert torch.equal(Y, dq(*w, g=g)[:, at].t())
+
+
+@pytest.mark.parametrize("bits,K", WIDE)
+def test_gemm_dgrad(bits, K):
+    N, g = 3, 128
+    w = wide_weights(N, K, g, bits, 3)
+    f, dq = (w4.gemm_dgrad, w4.dequantize) if bits == 4 else (w4.gemm8_dgrad, w4.dequantize8)
+    dX = f(torch.eye(N, dtype=torch.bfloat16, device="cuda")[:2].contiguous(), *w, g=g)
+    W = dq(*w, g=g)
+    assert all(torch.equal(dX[m], W[m]) for m in range(2))

@@ -837,14 +837,14 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
                             b -= per_product;
                             tp = &tmP1;
                         }
-                        const int c0 = (r0 + rank * 2 * kPairRows) * BITS / 8;   // code bytes; boxes of 128
+                        const int c0 = (r0 + rank * 2 * kPairRows) / (8 / BITS);   // code bytes; boxes of 128
 #pragma unroll
                         for (int h = 0; h < BITS / 4; ++h)
                             tma_load_2d(p + h * kPairBlock * 128, tp, c0 + 128 * h, b * kPairBlock, bar);
                     } else {
                         const int k = (walk.u0 + u) * UB * kPairBlock, n = r0 + rank * kPairRows;
-                        tma_load_2d(p, &tmP0, k * BITS / 8, n, bar);
-                        tma_load_2d(p + Cfg::kUnitBytes / 2, &tmP1, k * BITS / 8, n, bar);
+                        tma_load_2d(p, &tmP0, k / (8 / BITS), n, bar);
+                        tma_load_2d(p + Cfg::kUnitBytes / 2, &tmP1, k / (8 / BITS), n, bar);
                     }
                     ++issued;
                     if (++s == SP) { s = 0; ph ^= 1u; }

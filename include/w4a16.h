@@ -308,8 +308,9 @@ w4a16_status w8a16_gemm_plan(int64_t M, int64_t N, int64_t K, int32_t g, int32_t
  * deterministic.  M ≤ 16: the decode kernel with 8-bit codes (units of 256
  * rows x 128 K, i.e. the same 32 KB TMA tiles; each word of 4 codes becomes two
  * bf16 pairs — the code as a subnormal bf16 number, one exact fma to (q − z)·2^-6, the
- * product with s·2^6 rounded once; s below 2^122 — and feeds one mma.sync; split row
- * blocks are finished in the kernel, as for INT4).  M > 16: the tensor-core kernel with 8-bit
+ * product with s·2^6 rounded once; rows with s of 2^122 or more are summed anew in
+ * binary32 — and feeds one mma.sync; split row blocks are finished in the kernel, as for
+ * INT4).  M > 16: the tensor-core kernel with 8-bit
  * codes (64-byte code rows per K block, binary32-exact dequantization into the
  * shared-memory A tile, tcgen05 MMA), split-K as for INT4.  workspace: at least
  * w8a16_gemm_workspace_size() bytes, 16-byte aligned, when that is nonzero;
@@ -361,7 +362,8 @@ w4a16_status w8a8_gemm(const void* qx, const void* sx, int64_t M, int64_t K, con
  * Quantized weights are those of w4a16_quantize (w8a16_quantize for the w8a16_
  * forms): same layouts, g and K rules, alignment, stream and error conventions as
  * above, and the weight they stand for is the same Ŵ = bf16_rn((q − z)·s).
- * Scales are below 2^122 (those of weights up to about 2^125 are).
+ * Scales are below 2^122 (those of weights up to about 2^125 are), but for
+ * w4a16_gated and w8a16_gated on the decode path and the embeddings, which take any.
  * Every product is accumulated in binary32.  Results are deterministic.  Every
  * workspace is scratch: calls that may run at the same time (two streams, two
  * captured graphs) need two.  A call that follows one that gave up a wait

@@ -173,14 +173,24 @@ struct UnitWalk {
 // Tensor maps of a launch (GATED: P, S, Z of the gate projection, P2, S2, Z2 of the up one),
 // and the arguments that only GATED has.  (In DecodeArgs they changed the registers and the
 // schedule of the instances that do not use them: 70B-shaped layers 4% slower.)
-template <bool GATED>
+// RAW: the operands themselves too, for decode_wide_rows.
+template <bool GATED, bool RAW = true>
 struct DecodeMaps {
     CUtensorMap P, X, S, Z;
 };
 template <>
-struct DecodeMaps<true> {
+struct DecodeMaps<false, true> {
+    CUtensorMap P, X, S, Z;
+    const uint8_t* codes;
+    const uint16_t* x;
+};
+template <>
+struct DecodeMaps<true, true> {
     CUtensorMap P, X, S, Z, P2, S2, Z2;
-    const uint16_t* scales2;     // the up projection's
+    const uint8_t* codes;
+    const uint8_t* codes2;       // the up projection's
+    const uint16_t* x;
+    const uint16_t* scales2;
     const uint16_t* zeros2;
     uint16_t* G;                 // the projections' outputs, or null
     uint16_t* U;
@@ -281,8 +291,8 @@ __device__ __forceinline__ int unit_feature(int rb, int r) {
     return GATED ? rb * (kDecRows / 2) + (r & (kDecRows / 2 - 1)) : rb * kDecRows + r;
 }
 
-template <bool GATED>
-__device__ __forceinline__ const uint16_t* scale_base(const DecodeMaps<GATED>& maps, const DecodeArgs& a, int arr,
+template <bool GATED, bool RAW>
+__device__ __forceinline__ const uint16_t* scale_base(const DecodeMaps<GATED, RAW>& maps, const DecodeArgs& a, int arr,
                                                       int r) {
     if constexpr (GATED)
         if (r >= kDecRows / 2) return arr == 0 ? maps.scales2 : maps.zeros2;
@@ -292,8 +302,8 @@ __device__ __forceinline__ const uint16_t* scale_base(const DecodeMaps<GATED>& m
 // The producer's cp.async copies of a unit's scales (and zeros) when their rows
 // are not 16-byte aligned: per array and row, GU·2 bytes as copies of CS bytes,
 // lane l taking rows l, l + 32, ... (no integer division in the loop).
-template <int GU, int CS, bool GATED>
-__device__ __forceinline__ void copy_scale_rows(const DecodeMaps<GATED>& maps, const DecodeArgs& a, uint32_t sz,
+template <int GU, int CS, bool GATED, bool RAW>
+__device__ __forceinline__ void copy_scale_rows(const DecodeMaps<GATED, RAW>& maps, const DecodeArgs& a, uint32_t sz,
                                                 int sz_array, int rb, int g0, int arrays, int lane) {
     constexpr int kPerRow = (GU * 2 + CS - 1) / CS;
     for (int arr = 0; arr < arrays; ++arr) {
@@ -335,7 +345,7 @@ __device__ __forceinline__ void decode_store_y(const DecodeArgs& a, const float 
 // tokens 8mb + 2q and + 1.  H is rounded once, from the binary32 sums; G and U, when
 // they are kept for a backward pass, are rounded apart.
 template <int MB>
-__device__ __forceinline__ void decode_store_gated(const DecodeMaps<true>& maps, const DecodeArgs& a,
+__device__ __forceinline__ void decode_store_gated(const DecodeMaps<true, true>& maps, const DecodeArgs& a,
                                                    const float (&d)[MB][4], int rb, int w, int g, int q) {
     const int n = rb * (kDecRows / 2) + 8 * w + g;
 #pragma unroll
@@ -358,7 +368,7 @@ __device__ __forceinline__ void decode_store_gated(const DecodeMaps<true>& maps,
 // bf16_rn((q − z)·s).  A byte q alone in a 16-bit half is, as bf16, q·2^-133 exactly
 // (subnormal, or in the first normal binade, which continues the same steps); one fma
 // with 2^127 and nz = −z·2^-6 gives (q − z)·2^-6 exactly (an integer of at most 8 bits),
-// and the product with s6 = s·2^6 rounds (q − z)·s once (exact while s < 2^122).  Six
+// and the product with s6 = s·2^6 rounds (q − z)·s once (s < 2^122; see decode_wide_rows).  Six
 // instructions; placing bytes in binary32 mantissas took fourteen.  Symmetric words are
 // XORed with 0x80808080 by the caller (offset-128 codes, nz = −2).
 __device__ __forceinline__ void dq_word8(uint32_t w, uint32_t s6, uint32_t nz, uint32_t& lo, uint32_t& hi) {
@@ -380,9 +390,54 @@ __device__ __forceinline__ uint32_t dq_pair4(uint32_t w, uint32_t mask, uint32_t
     return bf16x2_mul(bf16x2_fma(c, POS ? 0x7D007D00u : 0x7F007F00u, nz), s6);
 }
 
+// Where codes are dequantized with s·2^6, a scale of 2^122 or more has none.  The main loop only
+// keeps the largest scale of a warp's rows, and when it was as large as that their sums are formed
+// anew here, from the operands in memory with the definition itself, in binary32: any finite weight
+// counts, whatever the time.  (Testing each unit, with a second form of its products beside the
+// first, cost 2 to 6% at every size: 28672 x 8192, 8 bits, M = 1: 46.4 us instead of 45.5.)
+// d[mb][2hr + j]: row 8 (GATED: 128) x hr further, token 8mb + 2q + j, K blocks [kb0, kb1).
+constexpr uint32_t kDecWideScale = 0x7C80u;                     // 2^122 as bf16
+template <int MB, bool SYM, int G, int BITS, bool GATED>
+__device__ __forceinline__ void decode_wide_rows(const DecodeMaps<GATED, true>& maps, const DecodeArgs& a, int rb,
+                                                 int kb0, int kb1, int w, int g, int q, float (&d)[MB][4]) {
+    const int k1 = min((int64_t)kb1 * dec_block_k<BITS>(), (int64_t)a.K);
+#pragma unroll
+    for (int hr = 0; hr < 2; ++hr) {
+        const int r = GATED ? 8 * w + g + hr * (kDecRows / 2) : 16 * w + g + 8 * hr;
+        const int n = unit_feature<GATED>(rb, r);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) d[mb][2 * hr] = d[mb][2 * hr + 1] = 0.0f;
+        if (n >= a.N) continue;
+        const uint8_t* codes = maps.codes;
+        if constexpr (GATED)
+            if (hr) codes = maps.codes2;
+        codes += (int64_t)n * a.K / (8 / BITS);
+        const uint16_t* sp = scale_base<GATED>(maps, a, 0, r) + (int64_t)n * a.Gtot;
+        const uint16_t* zp = SYM ? sp : scale_base<GATED>(maps, a, 1, r) + (int64_t)n * a.Gtot;
+#pragma unroll 1
+        for (int k = kb0 * dec_block_k<BITS>(); k < k1; ++k) {
+            const int grp = G == 0 ? 0 : k / (G == 0 ? 1 : G);
+            int c;
+            if constexpr (BITS == 4) c = codes[k >> 1] >> (4 * (k & 1)) & 15;
+            else c = codes[k];
+            if (SYM) c = (c ^ (1 << (BITS - 1))) - (1 << (BITS - 1));
+            const float z = SYM ? 0.0f : bf16_bits_to_f32(zp[grp]);
+            const float wv = __uint_as_float(f32_to_bf16_bits_rn(((float)c - z) * bf16_bits_to_f32(sp[grp])) << 16);
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int m = 8 * mb + 2 * q + j;
+                    if (m < a.M) d[mb][2 * hr + j] += wv * bf16_bits_to_f32(maps.x[(int64_t)m * a.K + k]);
+                }
+        }
+    }
+}
+
 template <int MB, bool SYM, int G, int BITS, bool GATED = false>
 __global__ void __launch_bounds__(kDecThreads, 1)
-    gemv_decode_kernel(const __grid_constant__ DecodeMaps<GATED> maps, const DecodeArgs a) {
+    gemv_decode_kernel(const __grid_constant__ DecodeMaps<GATED, GATED || BITS == 8> maps, const DecodeArgs a) {
+    constexpr bool kScaled = GATED || BITS == 8;                // codes are dequantized with s·2^6
     constexpr int kBoxRows = GATED ? kDecRows / 2 : kDecRows;   // rows per TMA box
     // G == 0: per-channel granularity, one scale (and zero) per row for all of K.
     constexpr int BK = dec_block_k<BITS>();            // K per unit
@@ -781,6 +836,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     int s = 0;
     uint32_t ph = 0;
     const uint8_t* stp = smem;
+    uint32_t largest = 0u;                  // kScaled: the row block's largest scales, two of a word
     for (int sg = 0; sg < nseg; ++sg) {
         int rb, kb0, kb1;
         if (sg == 0) {
@@ -821,12 +877,26 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                         slab_ptr = slab_base + slab_slot * kDecSlabBytes;
                         slab_rb = rb;
                         slab_j = j;
+                        // (the four lanes of a row look at two of its eight groups each)
+                        if constexpr (kScaled)
+#pragma unroll
+                            for (int hr = 0; hr < 2; ++hr)
+                                largest = __vmaxu2(largest, 0x7FFF7FFFu & *reinterpret_cast<const uint32_t*>(
+                                                                              slab_ptr + srow0 + hr * srow8 + 4 * q));
                     }
                     // the unit's groups start at (kb·GU) mod 8 within a slab row
                     sb = slab_ptr + srow0 + ((kb * GU) & 7) * 2;
                 } else {
                     // (pair copies: the unit's group is the half g0 mod 2 of its 4 bytes)
                     sb = stp + a.sz_off + srow0 + (a.sz_copy == 3 ? ((kb * GU) & 1) * 2 : 0);
+                    if constexpr (kScaled)
+                        if (G != 0 || kb == kb0)
+#pragma unroll
+                            for (int hr = 0; hr < 2; ++hr)
+                                largest = __vmaxu2(
+                                    largest, 0x7FFF7FFFu & (*reinterpret_cast<const uint16_t*>(sb + sgrp0 * 2 + hr * srow8) |
+                                                            (uint32_t)*reinterpret_cast<const uint16_t*>(
+                                                                sb + sgrp1 * 2 + hr * srow8) << 16));
                 }
                 if (have) {
                 if constexpr (BITS == 4) {
@@ -965,6 +1035,11 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                 acc[1][mb][j] = 0.0f;
             }
         if (*abort_flag != 0) continue;
+        if constexpr (kScaled) {
+            if (__any_sync(0xffffffffu, (largest >> 16) >= kDecWideScale || (largest & 0xFFFFu) >= kDecWideScale))
+                decode_wide_rows<MB, SYM, G, BITS, GATED>(maps, a, rb, kb0, kb1, w, g, q, d);
+            largest = 0u;
+        }
         // The row block is whole here iff all its units lie in this CTA's range.
         const int64_t first_u = (int64_t)rb * a.KBn;
         const bool whole = first_u >= u0 && first_u + a.KBn <= u1;

@@ -178,7 +178,7 @@ PairPlan dgrad_plan(int64_t M, int64_t N, int64_t K, int products) {
 
 // ---------------------------------------------------------------- gated, decode form
 template <int MB, bool SYM, int G, int BITS>
-w4a16_status launch_gated_decode_t(int64_t grid, int smem, const DecodeMaps<true>& maps, const DecodeArgs& args,
+w4a16_status launch_gated_decode_t(int64_t grid, int smem, const DecodeMaps<true, true>& maps, const DecodeArgs& args,
                                    cudaStream_t stream) {
     auto kern = gemv_decode_kernel<MB, SYM, G, BITS, true>;
     static bool done[kMaxDevices] = {};
@@ -202,7 +202,7 @@ w4a16_status launch_gated_decode_t(int64_t grid, int smem, const DecodeMaps<true
 }
 
 template <int MB, bool SYM, int BITS>
-w4a16_status launch_gated_decode_g(int gsel, int64_t grid, int smem, const DecodeMaps<true>& maps,
+w4a16_status launch_gated_decode_g(int gsel, int64_t grid, int smem, const DecodeMaps<true, true>& maps,
                                    const DecodeArgs& args, cudaStream_t stream) {
     switch (gsel) {
         case 32: return launch_gated_decode_t<MB, SYM, 32, BITS>(grid, smem, maps, args, stream);
@@ -264,7 +264,10 @@ w4a16_status launch_gated_decode(const GatedPlan& q, const void* X, int64_t M, i
     const uint64_t row_bytes = (uint64_t)K * bits / 8;
     const bool pc = per_channel(g, K);
     const uint64_t groups = pc ? 1 : (uint64_t)(K / g);
-    DecodeMaps<true> maps;
+    DecodeMaps<true, true> maps;
+    maps.codes = static_cast<const uint8_t*>(w[0].codes);
+    maps.codes2 = static_cast<const uint8_t*>(w[1].codes);
+    maps.x = static_cast<const uint16_t*>(X);
     w4a16_status st = encode_rows(&maps.P, CU_TENSOR_MAP_DATA_TYPE_UINT8, w[0].codes, row_bytes, (uint64_t)N, row_bytes,
                                   kDecUnitRowBytes, kDecRows / 2, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st == W4A16_OK)

@@ -150,7 +150,7 @@ w4a16_status make_plan(int64_t M, int64_t N, int64_t K, int32_t g, int32_t sym, 
 
 // ---------------------------------------------------------------- decode launch
 template <int MB, bool SYM, int G, int BITS>
-w4a16_status launch_decode_t(const w4a16_plan& p, const DecodeMaps<false>& maps,
+w4a16_status launch_decode_t(const w4a16_plan& p, const DecodeMaps<false, BITS == 8>& maps,
                              const DecodeArgs& args, cudaStream_t stream) {
     auto kern = gemv_decode_kernel<MB, SYM, G, BITS>;
     static bool attr_set[kMaxDevices] = {};
@@ -231,14 +231,15 @@ w4a16_status launch_decode(const w4a16_plan& p, const void* X, int64_t M, int64_
     }
     args.early = static_weights ? 1 : 0;
     args.units = d.units;
-    const DecodeMaps<false> maps{tmP, tmX, tmS, tmZ};
+    const DecodeMaps<false, false> maps4{tmP, tmX, tmS, tmZ};
+    const DecodeMaps<false, true> maps8{tmP, tmX, tmS, tmZ, static_cast<const uint8_t*>(packed), static_cast<const uint16_t*>(X)};
     const int gsel = pc ? 0 : g;                   // kernel group size, 0 = per-channel
 #define W4A16_DEC_G(MBV, SYMV, BV)                                                              \
     switch (gsel) {                                                                             \
-        case 32: return launch_decode_t<MBV, SYMV, 32, BV>(p, maps, args, stream);   \
-        case 64: return launch_decode_t<MBV, SYMV, 64, BV>(p, maps, args, stream);   \
-        case 128: return launch_decode_t<MBV, SYMV, 128, BV>(p, maps, args, stream); \
-        case 0: return launch_decode_t<MBV, SYMV, 0, BV>(p, maps, args, stream);     \
+        case 32: return launch_decode_t<MBV, SYMV, 32, BV>(p, maps##BV, args, stream);   \
+        case 64: return launch_decode_t<MBV, SYMV, 64, BV>(p, maps##BV, args, stream);   \
+        case 128: return launch_decode_t<MBV, SYMV, 128, BV>(p, maps##BV, args, stream); \
+        case 0: return launch_decode_t<MBV, SYMV, 0, BV>(p, maps##BV, args, stream);     \
         default: return W4A16_EINVAL;                                                           \
     }
 #define W4A16_DEC_MS(BV)                      \

@@ -363,7 +363,9 @@ w4a16_status w8a8_gemm(const void* qx, const void* sx, int64_t M, int64_t K, con
  * forms): same layouts, g and K rules, alignment, stream and error conventions as
  * above, and the weight they stand for is the same Ŵ = bf16_rn((q − z)·s).
  * Scales are below 2^122 (those of weights up to about 2^125 are), but for
- * w4a16_gated and w8a16_gated on the decode path and the embeddings, which take any.
+ * w4a16_gated and w8a16_gated on the decode path and the embeddings, which take any:
+ * a call that meets a larger one in what it multiplies sets W4A16_DEVERR_SCALE in the
+ * device error word, and its results are infinities or NaNs where that scale enters.
  * Every product is accumulated in binary32.  Results are deterministic.  Every
  * workspace is scratch: calls that may run at the same time (two streams, two
  * captured graphs) need two.  A call that follows one that gave up a wait
@@ -480,11 +482,12 @@ w4a16_status w4a16_embedding_grad(const void* dY, const void* ids, int32_t id_by
 /* Device error word: the kinds of report that kernels made, one bit each. */
 #define W4A16_DEVERR_WAIT 1   /* a bounded wait was given up */
 #define W4A16_DEVERR_ID 2     /* an embedding met an id not below the table's rows */
+#define W4A16_DEVERR_SCALE 4  /* a tensor-core gated block or a dX met a scale of 2^122 or more */
 
 /* Read and clear the current device's error word, written by a kernel that gave
  * up a bounded wait (a pipeline barrier that did not complete within about one
- * second) or met a bad id: W4A16_DEVERR_*, OR'ed when both happened.  *code = 0 when no
- * kernel reported one.
+ * second), met a bad id or a scale that it cannot take: W4A16_DEVERR_*, OR'ed when
+ * several happened.  *code = 0 when no kernel reported one.
  * Synchronizes the device. */
 w4a16_status w4a16_device_error(int32_t* code);
 

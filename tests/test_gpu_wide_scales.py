@@ -73,3 +73,72 @@ def test_gated_decode(exponent, M, g, bits, sym):
         W = dq(*w, g=g or K, sym=sym)
         assert bool(W.isfinite().all())
         assert torch.equal(Y, W[:, at].t())
+
+
+TAKEN = [e for e in EXPONENTS if e < 122]
+
+
+@pytest.mark.parametrize("exponent", EXPONENTS)
+@pytest.mark.parametrize("M", [40, 90, 200])
+@pytest.mark.parametrize("g", [32, 64, 128, 0])
+@pytest.mark.parametrize("bits,sym", [(4, False), (4, True), (8, False), (8, True)])
+def test_gated_tensor_cores(exponent, M, g, bits, sym):
+    """Exact below 2^122; from there on the call says that it met such a scale."""
+    N, K = 300, 1152
+    gate, up = weights(N, K, g or K, bits, sym, exponent, M), weights(N, K, g or K, bits, sym, -5, M + 50)
+    f, dq = (w4.gated, w4.dequantize) if bits == 4 else (w4.gated8, w4.dequantize8)
+    X, at = one_hot(M, K)
+    for a, b in ((gate, up), (up, gate)):
+        _, G, U = f(X, a, b, g=g or K, sym=sym, act="relu", save=True)
+        if exponent not in TAKEN:
+            assert w4.device_error() == 4
+            continue
+        for Y, w in ((G, a), (U, b)):
+            W = dq(*w, g=g or K, sym=sym)
+            assert bool(W.isfinite().all())
+            assert torch.equal(Y, W[:, at].t())
+
+
+@pytest.mark.parametrize("exponent", EXPONENTS)
+@pytest.mark.parametrize("N", [40, 300])
+@pytest.mark.parametrize("g", [32, 64, 128, 0])
+@pytest.mark.parametrize("bits,sym", [(4, False), (4, True), (8, False), (8, True)])
+def test_gemm_dgrad(exponent, N, g, bits, sym):
+    K = 1152
+    w = weights(N, K, g or K, bits, sym, exponent, N)
+    f, dq = (w4.gemm_dgrad, w4.dequantize) if bits == 4 else (w4.gemm8_dgrad, w4.dequantize8)
+    W = dq(*w, g=g or K, sym=sym)
+    assert bool(W.isfinite().all())
+    eye = torch.eye(N, dtype=torch.bfloat16, device="cuda")
+    for rows in (eye, eye[:17].contiguous()):
+        dX = f(rows, *w, g=g or K, sym=sym)
+        if exponent not in TAKEN:
+            assert w4.device_error() == 4
+        else:
+            assert torch.equal(dX, W[:rows.shape[0]])
+
+
+def test_one_wide_scale_is_enough():
+    """Wherever it stands: first and last row, first and last group, gate or up, one product of two."""
+    N, K, g, M = 300, 1152, 64, 40
+    gate, up = weights(N, K, g, 4, False, -5, 1), weights(N, K, g, 4, False, -5, 2)
+    X, _ = one_hot(M, K)
+    dH = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    w4.gated(X, gate, up, g=g)
+    w4.gated_backward(dH, dH, dH, gate, up, g=g)
+    assert w4.device_error() == 0
+    for n in (0, 131, N - 1):
+        for j in (0, 7, K // g - 1):
+            for which in range(2):
+                pair = [gate, up]
+                s = pair[which][1].clone()
+                s[n, j] = 2.0 ** 122
+                pair[which] = (pair[which][0], s, pair[which][2])
+                w4.gated(X, *pair, g=g)
+                assert w4.device_error() == 4
+                w4.gated_backward(dH, dH, dH, *pair, g=g)
+                assert w4.device_error() == 4
+                w4.gemm_dgrad(dH, *pair[which], g=g)
+                assert w4.device_error() == 4
+                w4.gated(X[:8].contiguous(), *pair, g=g)      # the decode path takes it
+                assert w4.device_error() == 0

@@ -583,7 +583,8 @@ def linear_w8a8(X: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,
 
 def device_error() -> int:
     """Read and clear the device error word, a set of bits (0: nothing; 1: a kernel gave up a
-    bounded wait; 2: an embedding met an id not below its table's rows)."""
+    bounded wait; 2: an embedding met an id not below its table's rows; 4: the gated block on
+    the tensor cores, or a dX, met a scale of 2^122 or more)."""
     code = ctypes.c_int32(0)
     _check(lib().w4a16_device_error(ctypes.byref(code)), "w4a16_device_error")
     return int(code.value)

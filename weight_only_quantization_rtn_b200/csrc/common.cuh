@@ -21,6 +21,7 @@ namespace w4a16 {
 __device__ int g_device_error;
 
 constexpr int kErrMbarTimeout = 1;
+constexpr int kErrWideScale = 4;
 constexpr unsigned long long kWaitTimeoutNs = 1000000000ull;   // one second per wait
 
 __device__ __forceinline__ uint64_t global_timer_ns() {

@@ -142,3 +142,13 @@ def test_one_wide_scale_is_enough():
                 assert w4.device_error() == 4
                 w4.gated(X[:8].contiguous(), *pair, g=g)      # the decode path takes it
                 assert w4.device_error() == 0
+
+
+@pytest.mark.parametrize("exponent", EXPONENTS)
+@pytest.mark.parametrize("g", [32, 128, 0])
+@pytest.mark.parametrize("bits,sym", [(4, False), (4, True), (8, False), (8, True)])
+def test_embedding(exponent, g, bits, sym):
+    V, K = 70, 1152
+    w = weights(V, K, g or K, bits, sym, exponent, 9)
+    f, dq = (w4.embedding, w4.dequantize) if bits == 4 else (w4.embedding8, w4.dequantize8)
+    assert torch.equal(f(torch.arange(V, device="cuda"), *w, g=g or K, sym=sym), dq(*w, g=g or K, sym=sym))

@@ -1029,8 +1029,7 @@ __global__ void __launch_bounds__(PairConfig<PAIR, BITS, DGRAD>::kThreads, 1)
             cnt += nb;
             if (more) ucnt += walk.units;
             // The A tiles of a block are written: visible to the tensor core, then counted; the
-            // codes were used, so their slot is given back.  (Given back right behind the
-            // loads, a slot was seen refilled before a load of it had been performed.)
+            // codes were used, so their slot is given back.
             auto release = [&]() {
                 if constexpr (Cfg::kTmemA) {
                     tmem_wait_st();

@@ -18,6 +18,11 @@ quantized embedding with its table's gradient (``embedding``, ``embedding_grad``
     Y = gemm(H, *down)
     dH = gemm_dgrad(dY, *down)
     dX, dG, dU = gated_backward(dH, G, U, gate, up, act="silu")
+
+No call takes part in automatic differentiation: results carry no graph, also where the
+inputs require gradients, and a training step calls the backward passes itself (or wraps
+the pairs of calls in a torch.autograd.Function).  A result given as ``out`` must not
+overlap the inputs.
 """
 from __future__ import annotations
 

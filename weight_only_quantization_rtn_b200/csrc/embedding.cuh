@@ -4,7 +4,7 @@
 // A row is gathered as codes (0.53 bytes per weight with 4 bits), dequantized in
 // registers and written once: bound by writing the bf16 rows.  One thread per 8 codes, so
 // a warp reads 128 (256) contiguous code bytes and writes 512 contiguous bytes (8192 ids,
-// K = 8192, 8 bits: 34 us, 6.0 TB/s).
+// K = 8192, 8 bits: 36 to 39 us, 5.2 to 5.7 TB/s).
 //
 // Gradient:  dW[v, :] = scale·Σ_{t: id_t = v} dY[t, :], summed in binary32 in ascending t
 // within windows of 32 or 64 sorted tokens (by T alone), windows added in order: the same inputs
@@ -20,8 +20,8 @@
 // Most of the time goes to writing zeros into the rows that no token names.  Step 3 writes
 // most of them (it finds them in the sorted list); the first 30 MB are written beside the
 // sort, which leaves the machine idle (by CTAs that look through the ids themselves), the
-// last sixteenth beside step 4.  Table of 32000 rows, K = 4096: 2048 ids, bf16 53 us; 16384 ids,
-// binary32 127 us: both 5.2 TB/s.
+// last sixteenth beside step 4.  Table of 32000 rows, K = 4096: 2048 ids, bf16 56 us; 16384 ids,
+// binary32 127 us: 5.0 and 5.2 TB/s.
 // An id below 0 or not below V names no row: it sorts behind all others and is dropped.
 #pragma once
 

@@ -44,9 +44,10 @@
 // has usually been there for a while, nothing waits in a circle, and the epilogues of the
 // CTAs are spread over time instead of all writing at once.
 //
-// Measured (K = 4096, N = 11008, both 4-bit): M = 2048 with G and U kept 254 us = 1455 TFLOP/s, its
-// dX 236 us, bound by the tensor cores and, in longer runs, by the power limit; M = 61 31 us, bound
-// by dequantization (about 0.35 us per block and SM) and the join.
+// Measured on the device (K = 4096, N = 11008, both 4-bit): M = 2048 with G and U kept 265 us =
+// 1395 TFLOP/s in a short run and 305 to 317 us in a long one, bound by the tensor cores and then by
+// the power limit, its backward pass (with the elementwise half) 265 and 313 us; M = 61 29 us,
+// 13 to 16 us of it dequantization (0.35 to 0.44 us per block and SM).
 #pragma once
 
 #include "activation.cuh"

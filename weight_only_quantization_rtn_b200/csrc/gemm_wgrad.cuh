@@ -12,7 +12,8 @@
 // MMAs: a tile of 2048 tokens is only about 9 us of MMAs.  A warp's 32 rows x 64 channels leave
 // through shared memory as one TMA store of full 128-byte lines (a lane writing its own row
 // in 16-byte pieces took 65 us for M = 77, N = K = 8192, where writing dW is all there is to do;
-// so it takes 29).  M = 2048, N = 4096, K = 11008: 125 us, 1478 TFLOP/s.
+// so it takes 31).  M = 2048, N = 4096, K = 11008: 127 us, 1460 TFLOP/s, in a short run, 149 us in a
+// long one (power limit).
 #pragma once
 
 #include "gemm_pair.cuh"

@@ -67,8 +67,8 @@
 //    rows 8..15 the same features' up rows.  An accumulator fragment holds rows g and
 //    g + 8 of the tile, so each lane ends with G and U of the same feature and tokens
 //    and forms act(G)·U in registers, from binary32 sums: no exchange, and nothing but
-//    H (and G and U when they are kept) is written.  4 bits, M = 1, K = 4096, N = 11008: 19 us;
-//    M = 8, 8192 x 28672: 80 us, 3.0 TB/s; bound by instruction issue like the rest.
+//    H (and G and U when they are kept) is written.  4 bits, M = 1, K = 4096, N = 11008: 18 us
+//    on the device; M = 8, 8192 x 28672: 81 us, 3.0 TB/s; bound by instruction issue like the rest.
 #pragma once
 
 #include "activation.cuh"

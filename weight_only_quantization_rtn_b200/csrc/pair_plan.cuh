@@ -46,7 +46,9 @@ inline void pair_plan_args(const PairPlan& p, PairArgs* a) {
 // that the time is estimated for 1, 2, 3, ... sharers of each tile and for all CTAs, and the
 // least is taken: a block takes about 0.55 us per 256 tokens and at least 0.5 us, 0.35 us for a
 // single CTA (dequantization), a CTA writes or reads a part at about 80 GB/s, and 2 us go to
-// the flags (M = 61, K = 11008, N = 4096: 31 us shared, 67 us whole).
+// the flags (M = 61, K = 11008, N = 4096: 31 us shared, 67 us whole).  It ranks the choices; as a
+// time it is low, by the start, the last epilogue and the join's waits (gated, M = 61, N = 11008,
+// K = 4096: 17.5 us for 29).
 inline PairPlan pair_plan(int64_t M, int64_t rows, int rows_per_cta, int64_t blocks, int unit_blocks, int sm_count) {
     PairPlan p{};
     p.ctas = M > kPairMaxSingle ? 2 : 1;

@@ -268,10 +268,13 @@ def _workspace_bytes(dev: torch.device, M, N, K, g, sym, pid, ctas) -> int:
 
 def _workspace(dev: torch.device, nbytes: int, sid: int | None = None):
     """A scratch buffer per (device, stream), grown on demand; calls on one
-    stream never overlap, so they can share it.  ``sid``: the current stream's
-    handle when the caller has it already."""
+    stream never overlap, so they can share it.  A captured call gets memory of its own,
+    from its graph's pool: graphs captured on one stream may be replayed on several.
+    ``sid``: the current stream's handle when the caller has it already."""
     if nbytes == 0:
         return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
     key = (dev, torch.cuda.current_stream(dev).cuda_stream if sid is None else sid)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
@@ -286,7 +289,10 @@ _dev_bufs: dict = {}
 def _device_buffer(dev: torch.device, M: int, N: int, sid: int, tag: str = "y") -> torch.Tensor:
     """A device bf16 [M, N] buffer per (device, stream, shape, role) for calls
     whose operands live in host memory (``tag`` "x": the copied activations, "y":
-    the result); calls on one stream are ordered, so they can share it."""
+    the result); calls on one stream are ordered, so they can share it.  Captured calls have
+    their own, as in _workspace."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty((M, N), dtype=torch.bfloat16, device=dev)
     key = (dev, sid, M, N, tag)
     buf = _dev_bufs.get(key)
     if buf is None:
